@@ -11,7 +11,10 @@
  *
  * plus the load-time twin builder nvfp4_moe_transpose_u8, the load-time scale
  * check nvfp4_moe_check_scales and nvfp4_moe_append_shared, which brings a
- * shared expert into the same four steps.
+ * shared expert into the same four steps; and the operators that stand around
+ * the forward in a layer: nvfp4_moe_route_topk (the routing that step 1 takes),
+ * nvfp4_moe_add_rms_norm (residual, norm and 8-bit rows) and
+ * nvfp4_moe_int8_matmul (8-bit products of such rows).
  *
  * Launch order.  The kernels use programmatic dependent launch: each may start
  * while the previous kernel on the stream is still running and waits for it
@@ -516,6 +519,142 @@ NVFP4_MOE_API int nvfp4_moe_transpose_concat(const uint8_t* const* packed_parts,
                                              uint32_t k, uint32_t group_size, uint32_t stride,
                                              uint8_t* packed_out, uint8_t* scale_out,
                                              cudaStream_t stream);
+
+/*
+ * The operators around the forward in a transformer layer: the norm before it,
+ * the routing that feeds it, and the 8-bit products next to it.  The pages name
+ * no launcher for them; conventions (device pointers, streams, status codes,
+ * programmatic launch order) are those of the calls above.  None of them takes
+ * a workspace or keeps anything between calls.  num_tokens (num_rows) == 0
+ * launches nothing.
+ *
+ * Element types of their arguments.  F32 and BF16 are the types of tensors;
+ * INT8 (two's complement, codes -127..127 written) and E4M3 (finite "FN"
+ * variant) those of quantised rows.
+ */
+typedef enum {
+  NVFP4_MOE_BF16 = 0,
+  NVFP4_MOE_F32 = 1,
+  NVFP4_MOE_INT8 = 2,
+  NVFP4_MOE_E4M3 = 3
+} nvfp4_moe_type;
+
+typedef enum {
+  NVFP4_MOE_SCORE_SOFTMAX = 1, /* s = exp(l) / sum over the row's experts   */
+  NVFP4_MOE_SCORE_SIGMOID = 2  /* s = 1 / (1 + exp(-l))                     */
+} nvfp4_moe_score;
+
+/*
+ * A router (host struct, read during the call).
+ *   bias         DEVICE f32 [num_experts] added to the scores for the choice
+ *                only (balance), or NULL
+ *   num_groups   consecutive groups of num_experts / num_groups experts; 1: none
+ *   topk_groups  groups a token may choose from, 1..num_groups
+ *   group_top    a group's score: the sum of its 1 or 2 best choice values
+ *   score        nvfp4_moe_score
+ *   renormalize  non-zero: a token's weights are divided by their sum
+ *   scale        factor on every weight
+ */
+typedef struct {
+  const float* bias;
+  uint32_t num_experts;
+  uint32_t topk;
+  uint32_t num_groups;
+  uint32_t topk_groups;
+  uint32_t group_top;
+  int32_t score;
+  int32_t renormalize;
+  float scale;
+} nvfp4_moe_router;
+
+/*
+ * Routing: the topk experts of each token and their weights, as
+ * nvfp4_moe_route_sort, nvfp4_moe_blend and the forward calls take them.
+ *
+ *   logits        bf16 or f32 [num_tokens, num_experts], rows ld elements apart
+ *   topk_ids      i32 [num_tokens, topk]  out, contiguous: the chosen experts,
+ *                 best first
+ *   topk_weights  f32 [num_tokens, topk]  out: their scores (without bias),
+ *                 renormalised if asked, times scale
+ *
+ * A token's choice value of expert e is s[e] + bias[e], without a bias l[e]
+ * (the scores are monotone in it); with num_groups > 1 the topk_groups groups
+ * with the best group scores stay (without a bias and with group_top 1 the best
+ * logit is a group's score, with group_top 2 the sum of its two best scores);
+ * then the topk best choice values, compared exactly (rows that FP32 cannot
+ * order are ordered in FP64), ties to the lower index.  An expert whose logit is
+ * -infinity or NaN, or whose bias is, cannot be chosen (a masked expert; an
+ * all-masked row is a padding token); a logit of +infinity counts as the
+ * largest finite one.  Slots that no expert can fill hold id -1 and weight 0:
+ * nvfp4_moe_route_sort drops such pairs (its status word is then 1), and the
+ * blend adds nothing for them.
+ * ESHAPE: num_experts not in 1..1024, topk not in 1..32, num_groups not in
+ * 1..32 or not dividing num_experts, topk_groups not in 1..num_groups, group_top
+ * not 1 or 2 or above the group's size, topk > topk_groups * group size,
+ * ld < num_experts, num_tokens * topk > 1<<24.  EINVAL: NULL or overlapping
+ * pointers, unknown type or score, a scale that is not finite.
+ */
+NVFP4_MOE_API int nvfp4_moe_route_topk(const void* logits, int logits_type, uint64_t ld,
+                                       uint32_t num_tokens, const nvfp4_moe_router* router,
+                                       int32_t* topk_ids, float* topk_weights, cudaStream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, output in BF16, in 8 bits
+ * with one scale per row, or both.  Per row:
+ *
+ *   r = x + residual (x alone when residual is NULL)
+ *   residual_out = r rounded to the residual's type
+ *   y = r / sqrt(mean(r^2) + eps) * weight
+ *   out = y rounded to bf16
+ *   q_scale = max|y| / Q, q = y / q_scale rounded to nearest even,
+ *   Q = 127 (INT8) or 448 (E4M3)
+ *
+ * r, the mean and y are FP32; out and q are rounded once, from the unrounded r.
+ *
+ *   x             bf16 or f32 [num_rows, hidden], rows ldx elements apart
+ *   residual      bf16 or f32, rows ldr elements apart, or NULL
+ *   residual_out  the residual's type [num_rows, hidden], contiguous, or NULL
+ *   weight        bf16 or f32 [hidden]
+ *   out           bf16 bits [num_rows, hidden], contiguous, or NULL
+ *   q, q_scale    8-bit codes [num_rows, hidden] (contiguous) of q_type and f32
+ *                 [num_rows], or both NULL; at least one of out and q
+ * residual_out and out may be exactly x or residual (same address, element size
+ * and row distance); any other overlap is refused.  A row of zeros gives zeros
+ * and a scale of 0.  A NaN or infinity in a row makes its y (not its r) and its
+ * scale NaN; a row whose sum of squares passes the FP32 range gives zeros.
+ * ESHAPE: hidden not in 1..32768, ldx or ldr < hidden, num_rows >= 2^31.
+ * EINVAL: unknown type, eps not a positive finite number, NULL or overlapping
+ * pointers, q without q_scale or the other way round, residual_out without
+ * residual.
+ */
+NVFP4_MOE_API int nvfp4_moe_add_rms_norm(const void* x, int x_type, uint64_t ldx,
+                                         const void* residual, int residual_type, uint64_t ldr,
+                                         void* residual_out, const void* weight, int weight_type,
+                                         float eps, uint32_t num_rows, uint32_t hidden,
+                                         uint16_t* out, void* q, int q_type, float* q_scale,
+                                         cudaStream_t stream);
+
+/*
+ * Product of 8-bit integer matrices with a scale per token and per channel:
+ *
+ *   out[m, j] = x_scale[m] * w_scale[j] * sum_k x[m, k] * w[j, k] + bias[j]
+ *
+ *   x        i8 [num_tokens, k], rows ldx bytes apart, 16-byte aligned
+ *   x_scale  f32 [num_tokens]
+ *   w        i8 [n, k], contiguous, 16-byte aligned
+ *   w_scale  f32 [n]        bias  f32 [n] or NULL
+ *   out      bf16 or f32 [num_tokens, n], rows ldo elements apart
+ *
+ * The integer sums are exact, so the result does not depend on how the work is
+ * split; scales and bias are applied in FP32 and the result is rounded once.
+ * ESHAPE: k not a multiple of 16 in 16..131056, ldx < k or not a multiple of
+ * 16, ldo < n, n == 0.  EINVAL: unknown type, NULL or misaligned pointers, out
+ * overlapping an input.
+ */
+NVFP4_MOE_API int nvfp4_moe_int8_matmul(const int8_t* x, uint64_t ldx, const float* x_scale,
+                                        const int8_t* w, const float* w_scale, const float* bias,
+                                        void* out, int out_type, uint64_t ldo, uint32_t num_tokens,
+                                        uint32_t n, uint32_t k, cudaStream_t stream);
 
 /* Host helper: launch bound on active experts, min(num_experts, num_pairs). */
 NVFP4_MOE_API uint32_t nvfp4_moe_active_cap(uint32_t num_experts, uint32_t num_pairs);

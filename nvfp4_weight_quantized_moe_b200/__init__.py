@@ -11,6 +11,7 @@ from ._binding import (  # noqa: F401
     PATH_AUTO,
     PATH_DECODE,
     PATH_PREFILL,
+    SCORES,
     SHARD_COLUMN,
     SHARD_ROW,
     Buffers,
@@ -18,6 +19,7 @@ from ._binding import (  # noqa: F401
     LaunchOpts,
     NVFP4MoEError,
     active_cap,
+    add_rms_norm,
     append_shared,
     blend,
     check_scales,
@@ -30,7 +32,9 @@ from ._binding import (  # noqa: F401
     forward_nongated,
     gate_up_silu,
     gate_up_silu_ws,
+    int8_matmul,
     route_sort,
+    route_topk,
     shard_nvfp4,
     shard_nvfp4_into,
     shared_slots,
@@ -43,6 +47,7 @@ from ._binding import (  # noqa: F401
 )
 from .layer import (  # noqa: F401
     MoEBuffers,
+    MoERouter,
     NVFP4MoE,
     NVFP4Projection,
     all_reduce_out,

@@ -28,6 +28,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 c_void_p = ctypes.c_void_p
 c_u32 = ctypes.c_uint32
+c_u64 = ctypes.c_uint64
 c_int = ctypes.c_int
 
 
@@ -49,7 +50,19 @@ class Buffers(ctypes.Structure):
                 ("act", c_void_p), ("y", c_void_p), ("out_f32", c_void_p), ("out_bf16", c_void_p)]
 
 
+class Router(ctypes.Structure):
+    """nvfp4_moe_router."""
+    _fields_ = [("bias", c_void_p), ("num_experts", c_u32), ("topk", c_u32), ("num_groups", c_u32),
+                ("topk_groups", c_u32), ("group_top", c_u32), ("score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 PATH_AUTO, PATH_DECODE, PATH_PREFILL = 0, 1, 2
+# nvfp4_moe_score: how a router turns logits into scores.
+SCORES = {"softmax": 1, "sigmoid": 2}
+# nvfp4_moe_type: tensors, and rows of 8-bit codes.
+_FLOAT_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+_CODE_TYPES = {torch.int8: 2, torch.float8_e4m3fn: 3}
 # nvfp4_moe_activation: the activation of a non-gated expert.
 ACTIVATIONS = {"relu2": 1, "silu": 2}
 SHARD_COLUMN, SHARD_ROW = 0, 1
@@ -104,6 +117,13 @@ _sig = {
                                            c_void_p, c_void_p, c_void_p]),
     "nvfp4_moe_shard_nvfp4": (c_int, [c_void_p, c_void_p, c_u32, c_u32, c_u32, c_int, c_u32, c_u32,
                                       c_void_p, c_void_p, c_void_p]),
+    "nvfp4_moe_route_topk": (c_int, [c_void_p, c_int, c_u64, c_u32, ctypes.POINTER(Router), c_void_p,
+                                     c_void_p, c_void_p]),
+    "nvfp4_moe_add_rms_norm": (c_int, [c_void_p, c_int, c_u64, c_void_p, c_int, c_u64, c_void_p,
+                                       c_void_p, c_int, ctypes.c_float, c_u32, c_u32, c_void_p,
+                                       c_void_p, c_int, c_void_p, c_void_p]),
+    "nvfp4_moe_int8_matmul": (c_int, [c_void_p, c_u64, c_void_p, c_void_p, c_void_p, c_void_p,
+                                      c_void_p, c_int, c_u64, c_u32, c_u32, c_u32, c_void_p]),
     "nvfp4_moe_workspace_bytes": (ctypes.c_size_t, [c_u32, c_u32, c_u32, c_u32]),
     "nvfp4_moe_device_error": (c_int, [c_int]),
     "nvfp4_moe_wait_selftest": (c_int, [c_u32, c_int, c_void_p]),
@@ -444,3 +464,158 @@ def forward_nongated(x, topk_ids, topk_weights, up: ExpertTables, down: ExpertTa
         _ptr(topk_weights, torch.float32, "topk_weights"), up, down, ctypes.byref(buffers),
         m, k, num_experts, hidden, inter, _activation(activation), _opts(path, split, tiles, depth, staging),
         wp, wn, _stream(stream)))
+
+
+# --- the operators around the forward ------------------------------------------
+# Their rows may be strided views, and they run on the device of their tensors,
+# on that device's current stream unless one is given.
+
+def _rows(t: torch.Tensor, name: str):
+    """(rows, columns, elements between rows) of a 2-D tensor with unit inner stride."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: must be 2-D")
+    m, n = t.shape
+    if (n > 1 and t.stride(1) != 1) or (m > 1 and t.stride(0) < n):
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+    return m, n, t.stride(0) if m > 1 else n
+
+
+def _on(t: torch.Tensor, dev: int, name: str, dtype=None) -> int:
+    """The tensor's address, after checking its device and type."""
+    if t.get_device() != dev or not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor on the same device as the others")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _vector(t: torch.Tensor, n: int, dev: int, name: str, dtype=torch.float32) -> int:
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name}: must be a contiguous vector of {n} values")
+    return _on(t, dev, name, dtype)
+
+
+def _matrix(t: torch.Tensor, m: int, n: int, dev: int, name: str, dtype=None) -> int:
+    if t.shape != (m, n) or not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous [{m}, {n}]")
+    return _on(t, dev, name, dtype)
+
+
+def _float_type(t: torch.Tensor, name: str) -> int:
+    code = _FLOAT_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    return code
+
+
+def _launch(name: str, dev: int, stream, *args) -> None:
+    """Call the entry point with the tensors' device current."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        stream = _stream(stream)
+    fn = getattr(_lib, name)
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != 0:
+        raise NVFP4MoEError(name, status)
+
+
+def _cuda_device(t: torch.Tensor, name: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    return t.get_device()
+
+
+def route_topk(logits, topk_ids, topk_weights, *, score="softmax", bias=None, num_groups=1,
+               topk_groups=1, group_top=1, renormalize=True, scale=1.0, stream=None) -> None:
+    """nvfp4_moe_route_topk: the topk experts of each row of ``logits`` [M, E] (bf16 or
+    f32, rows may be strided) and their weights, into ``topk_ids`` (i32 [M, topk]) and
+    ``topk_weights`` (f32 [M, topk]), which the forward takes as they are.
+
+    ``bias`` (f32 [E]) is added to the scores for the choice only.  With
+    ``num_groups`` > 1 a token chooses among the experts of its ``topk_groups`` best
+    groups (by the sum of a group's ``group_top`` best values).  Experts with a
+    logit of -inf or NaN are never chosen; slots left over hold id -1, weight 0."""
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    dev = _cuda_device(logits, "logits")
+    kind = _float_type(logits, "logits")
+    m, e, ld = _rows(logits, "logits")
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids: must be [M, topk]")
+    k = topk_ids.shape[1]
+    ids = _matrix(topk_ids, m, k, dev, "topk_ids", torch.int32)
+    weights = _matrix(topk_weights, m, k, dev, "topk_weights", torch.float32)
+    b = None if bias is None else _vector(bias, e, dev, "bias")
+    router = Router(b, e, k, num_groups, topk_groups, group_top, SCORES[score],
+                    1 if renormalize else 0, scale)
+    _launch("nvfp4_moe_route_topk", dev, stream, logits.data_ptr(), kind, ld, m,
+            ctypes.byref(router), ids, weights)
+
+
+def add_rms_norm(x, weight, eps, *, out=None, residual=None, residual_out=None, q=None,
+                 q_scale=None, stream=None) -> None:
+    """nvfp4_moe_add_rms_norm: r = x + residual, y = r / rms(r) * weight over the rows of
+    ``x`` [M, H] (bf16 or f32, rows may be strided).
+
+    Outputs, each optional but ``out`` or ``q``: ``residual_out`` (r in the
+    residual's type), ``out`` (y in bf16), ``q`` with ``q_scale`` (y in int8 or
+    float8_e4m3fn codes, one f32 scale per row).  ``residual_out`` may be
+    ``residual`` itself."""
+    dev = _cuda_device(x, "x")
+    kind = _float_type(x, "x")
+    m, h, ldx = _rows(x, "x")
+    w = _vector(weight, h, dev, "weight", None)
+    w_kind = _float_type(weight, "weight")
+    r = r_out = None
+    r_kind = ldr = 0
+    if residual is not None:
+        r_kind = _float_type(residual, "residual")
+        rm, rh, ldr = _rows(residual, "residual")
+        if (rm, rh) != (m, h):
+            raise ValueError("residual: must have the shape of x")
+        r = _on(residual, dev, "residual")
+    if residual_out is not None:
+        if residual is None:
+            raise ValueError("residual_out given without residual")
+        r_out = _matrix(residual_out, m, h, dev, "residual_out", residual.dtype)
+    y = None if out is None else _matrix(out, m, h, dev, "out", torch.bfloat16)
+    codes = scales = None
+    q_kind = 0
+    if (q is None) != (q_scale is None):
+        raise ValueError("q and q_scale belong together")
+    if q is not None:
+        q_kind = _CODE_TYPES.get(q.dtype)
+        if q_kind is None:
+            raise TypeError(f"q: expected int8 or float8_e4m3fn, got {q.dtype}")
+        codes = _matrix(q, m, h, dev, "q")
+        scales = _vector(q_scale, m, dev, "q_scale")
+    _launch("nvfp4_moe_add_rms_norm", dev, stream, x.data_ptr(), kind, ldx, r, r_kind, ldr, r_out,
+            w, w_kind, eps, m, h, y, codes, q_kind, scales)
+
+
+def int8_matmul(x_q, x_scale, w_q, w_scale, out, *, bias=None, stream=None) -> None:
+    """nvfp4_moe_int8_matmul: out = (x_q w_q^T) * x_scale[:, None] * w_scale (+ bias), with
+    ``x_q`` int8 [M, K] (rows may be strided), ``w_q`` int8 [N, K], f32 scales [M] and
+    [N], f32 ``bias`` [N] or None, ``out`` bf16 or f32 [M, N] (rows may be strided).
+    K is a multiple of 16; the integer sums are exact."""
+    dev = _cuda_device(x_q, "x_q")
+    m, k, ldx = _rows(x_q, "x_q")
+    x = _on(x_q, dev, "x_q", torch.int8)
+    if w_q.dim() != 2:
+        raise ValueError("w_q: must be [N, K]")
+    n = w_q.shape[0]
+    w = _matrix(w_q, n, k, dev, "w_q", torch.int8)
+    xs = _vector(x_scale, m, dev, "x_scale")
+    ws = _vector(w_scale, n, dev, "w_scale")
+    b = None if bias is None else _vector(bias, n, dev, "bias")
+    kind = _float_type(out, "out")
+    om, on, ldo = _rows(out, "out")
+    if (om, on) != (m, n):
+        raise ValueError(f"out: must be [{m}, {n}]")
+    _launch("nvfp4_moe_int8_matmul", dev, stream, x, ldx, xs, w, ws, b, _on(out, dev, "out"), kind,
+            ldo, m, n, k)

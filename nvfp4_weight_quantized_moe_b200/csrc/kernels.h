@@ -108,6 +108,57 @@ cudaError_t launch_blend(const float* y, const float* topk_weights, const int32_
                          float* out_f32, uint16_t* out_bf16, uint32_t num_tokens, uint32_t topk,
                          uint32_t hidden, cudaStream_t stream);
 
+// Routing of tokens to experts (route_topk.cu).  Logits are FP32 or BF16 rows
+// of num_experts, ld elements apart; one lane of a warp holds one choice and one
+// group, hence the two limits.
+constexpr uint32_t kMaxRouteTopk = 32;
+constexpr uint32_t kMaxRouteGroups = 32;
+struct RouterConfig {
+  const float* bias;
+  uint32_t num_experts, topk, num_groups, topk_groups, group_top;
+  bool softmax, renormalize;
+  float scale;
+};
+cudaError_t launch_route_topk(const void* logits, bool logits_f32, uint64_t ld, uint32_t num_tokens,
+                              const RouterConfig& r, int32_t* ids, float* weights, cudaStream_t stream);
+
+// RMS norm with the residual's addition (add_rms_norm.cu).  A row stays in the
+// registers of one CTA: 1024 threads of 32 values.
+constexpr uint32_t kMaxNormHidden = 32768;
+enum { kQuantNone = 0, kQuantInt8 = 1, kQuantE4M3 = 2 };
+struct NormConfig {
+  const void* x;
+  const void* residual;  // or NULL
+  void* residual_out;    // or NULL
+  const void* weight;
+  uint16_t* out;         // or NULL
+  void* q;               // or NULL
+  float* q_scale;
+  uint64_t ldx, ldr;     // elements between rows of x and of residual
+  uint32_t rows, hidden;
+  int q_kind;
+  bool x_f32, residual_f32, weight_f32;
+  float eps;
+};
+cudaError_t launch_add_rms_norm(const NormConfig& c, cudaStream_t stream);
+
+// Product of 8-bit integer matrices (int8_matmul.cu): x [M, K] rows ldx bytes
+// apart, w [N, K] contiguous, out [M, N] rows ldo elements apart.  A sum of K
+// products of at most 2^14 stays below 2^31 up to kMaxInt8K.
+constexpr uint32_t kMaxInt8K = 131056;
+struct Int8MatmulArgs {
+  const void* x;
+  const float* x_scale;
+  const void* w;
+  const float* w_scale;
+  const float* bias;  // or NULL
+  void* out;
+  uint64_t ldx, ldo;
+  uint32_t M, N, K;
+  bool out_f32;
+};
+cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, cudaStream_t stream);
+
 cudaError_t launch_append_shared(const int32_t* ids, const float* w, const float* shared_w,
                                  int32_t* ids_out, float* w_out, uint32_t num_tokens,
                                  uint32_t topk, uint32_t num_experts, uint32_t shared_rows,

@@ -105,12 +105,42 @@ class NVFP4Projection:
         return NVFP4Projection(packed, scale, self.scale2.clone(), null_experts=null)
 
 
+class MoERouter:
+    """How a layer's tokens choose their experts (:func:`route_topk`).
+
+    ``score`` ("softmax" or "sigmoid") of the logits, plus ``bias`` (f32 [E], device) for
+    the choice only; with ``num_groups`` > 1 the choice is among the ``topk_groups``
+    groups with the largest sum of their ``group_top`` (1 or 2) best values; weights
+    are the chosen scores, divided by their sum with ``renormalize``, times ``scale``.
+    """
+
+    def __init__(self, topk: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+                 num_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
+                 renormalize: bool = True, scale: float = 1.0):
+        if score not in B.SCORES:
+            raise ValueError(f"score must be one of {sorted(B.SCORES)}")
+        self.topk, self.score, self.bias = int(topk), score, bias
+        self.num_groups, self.topk_groups, self.group_top = num_groups, topk_groups, group_top
+        self.renormalize, self.scale = bool(renormalize), float(scale)
+
+    def route(self, logits: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
+              stream=None) -> None:
+        """The routing of ``logits`` [M, E] into topk_ids (i32) and topk_weights (f32) [M, topk]."""
+        if topk_ids.shape[1] != self.topk:
+            raise ValueError("topk_ids must be [M, topk]")
+        B.route_topk(logits, topk_ids, topk_weights, score=self.score, bias=self.bias,
+                     num_groups=self.num_groups, topk_groups=self.topk_groups,
+                     group_top=self.group_top, renormalize=self.renormalize, scale=self.scale,
+                     stream=stream)
+
+
 class MoEBuffers:
     """Outputs and intermediates of one forward, for M tokens.
 
     With a shared expert, ``topk`` and ``num_experts`` count its slot and
     table entries, and ``topk_ids`` / ``topk_weights`` hold the appended
-    routing [M, topk] that nvfp4_moe_append_shared writes.
+    routing [M, topk] that nvfp4_moe_append_shared writes.  ``routed_ids`` /
+    ``routed_weights`` hold the routing that :meth:`NVFP4MoE.forward_logits` computes.
     """
 
     def __init__(self, num_tokens: int, topk: int, num_experts: int, hidden: int, inter: int,
@@ -121,6 +151,9 @@ class MoEBuffers:
         self.num_tokens, self.topk = num_tokens, topk
         self.topk_ids = torch.empty(max(num_tokens, 1), topk, **i32) if shared else None
         self.topk_weights = torch.empty(max(num_tokens, 1), topk, **f32) if shared else None
+        routed = topk - 1 if shared else topk
+        self.routed_ids = torch.empty(max(num_tokens, 1), routed, **i32)
+        self.routed_weights = torch.empty(max(num_tokens, 1), routed, **f32)
         self.expert_offsets = torch.empty(num_experts + 1, **i32)
         self.sorted_pair_ids = torch.empty(max(p, 1), **i32)
         self.pair_pos = torch.empty(max(p, 1), **i32)
@@ -329,6 +362,25 @@ class NVFP4MoE:
                       workspace, **opts)
         B.blend(bufs.y, topk_weights, bufs.pair_pos, bufs.out, bufs.out_bf16, stream=stream)
         return bufs
+
+    def forward_logits(self, x: torch.Tensor, logits: torch.Tensor, router: MoERouter,
+                       bufs: Optional[MoEBuffers] = None, stream=None, **options) -> MoEBuffers:
+        """:meth:`forward` from the router's logits [M, E] (bf16 or f32): the routing is one
+        more launch, its result in ``bufs.routed_ids`` / ``bufs.routed_weights`` (first M
+        rows).  A token whose logits are all -inf (padding) adds nothing to ``out``.
+        ``options`` as for :meth:`forward`."""
+        m = x.shape[0]
+        if tuple(logits.shape) != (m, self.num_experts):
+            raise ValueError("logits must be [M, num_experts]")
+        if router.topk != self.topk:
+            raise ValueError("the router's topk differs from the layer's")
+        if bufs is None:
+            bufs = self.buffers(m)
+        if m > bufs.num_tokens:
+            raise ValueError("buffers were sized for fewer tokens")
+        ids, weights = bufs.routed_ids[:m], bufs.routed_weights[:m]
+        router.route(logits, ids, weights, stream=stream)
+        return self.forward(x, ids, weights, bufs, stream=stream, **options)
 
     def _forward_nongated(self, x, topk_ids, topk_weights, bufs, path, split, tiles, depth,
                           staging, workspace, stream, steps, shared_weights) -> MoEBuffers:
