@@ -219,9 +219,10 @@ size_t nvfp4_moe_workspace_bytes(uint32_t num_tokens, uint32_t topk, uint32_t hi
 }
 
 int nvfp4_moe_device_error(int clear) {
-  int v = 0;
-  if (read_device_error(&v, clear != 0) != cudaSuccess) return -1;
-  return v;
+  int grouped = 0, int8 = 0;
+  if (read_grouped_error(&grouped, clear != 0) != cudaSuccess) return -1;
+  if (read_int8_error(&int8, clear != 0) != cudaSuccess) return -1;
+  return grouped | int8;
 }
 
 int nvfp4_moe_wait_selftest(uint32_t cycle_limit, int arrive, cudaStream_t stream) {

@@ -55,6 +55,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_common.cuh"
+#include "tensor_map.h"
 
 namespace nvm {
 
@@ -725,37 +726,6 @@ __global__ void __launch_bounds__(kThreads) __maxnreg__(NT <= 16 ? 80 : 168)
 
 namespace {
 
-// cuTensorMapEncodeTiled from the driver, looked up once through the runtime.
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static std::once_flag once;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
-// Row-major 2-D tensor [rows, cols] of `elem`-byte elements at `base`; box
-// [box_rows, box_cols]; out-of-range rows read as zero.
-cudaError_t make_map_2d(CUtensorMap* map, const void* base, CUtensorMapDataType type, uint32_t elem,
-                        uint64_t rows, uint64_t cols, uint32_t box_rows, uint32_t box_cols,
-                        CUtensorMapSwizzle swizzle) {
-  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (fn == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * elem};
-  const cuuint32_t box[2] = {box_cols, box_rows};
-  const cuuint32_t estride[2] = {1, 1};
-  const CUresult r = fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estride,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <int MODE, int NT>
 cudaError_t launch_tc_impl(const TcArgs& a, const CUtensorMap& b0, const CUtensorMap& b1, uint32_t cap,
                            cudaStream_t stream) {
@@ -947,11 +917,6 @@ cudaError_t launch_wait_selftest(uint32_t cycle_limit, int arrive, cudaStream_t 
   return cudaGetLastError();
 }
 
-cudaError_t read_device_error(int* value, bool clear) {
-  cudaError_t err = cudaMemcpyFromSymbol(value, g_device_error, sizeof(int));
-  if (err != cudaSuccess || !clear) return err;
-  const int zero = 0;
-  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
-}
+cudaError_t read_grouped_error(int* value, bool clear) { return read_error_word(&g_device_error, value, clear); }
 
 }  // namespace nvm

@@ -475,13 +475,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, NT > 3
 
 namespace {
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2) return 148;
-  return n;
-}
-
 // Persistent launch: one pair per two SMs (two at 32-row passes), or fewer
 // when there are fewer tasks than that.
 template <int MODE, int NT>

@@ -95,7 +95,9 @@ size_t tc_workspace_bytes(uint64_t tokens, uint64_t topk, uint64_t hidden, uint6
 size_t tc_gate_up_workspace_bytes(uint64_t pairs, uint64_t hidden);
 cudaError_t launch_tc(int mode, int nt, const GroupedArgs& a, void* workspace, uint32_t tokens,
                       uint32_t hidden, uint32_t inter, uint32_t cap, cudaStream_t stream);
-cudaError_t read_device_error(int* value, bool clear);
+// The device error words of the files that wait on barriers.
+cudaError_t read_grouped_error(int* value, bool clear);
+cudaError_t read_int8_error(int* value, bool clear);
 // One bounded barrier wait on the device (self-test of the timeout path).
 cudaError_t launch_wait_selftest(uint32_t cycle_limit, int arrive, cudaStream_t stream);
 
@@ -158,6 +160,10 @@ struct Int8MatmulArgs {
   bool out_f32;
 };
 cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, cudaStream_t stream);
+// Its tensor-core forms (int8_matmul_tc.cu): 128 x bn tiles (bn 64 or 128) with K
+// split over a cluster of `split` CTAs (1, 2, 4, 8); 256 x 256 tiles by CTA pairs.
+cudaError_t launch_int8_tile(const Int8MatmulArgs& a, int bn, uint32_t split, cudaStream_t stream);
+cudaError_t launch_int8_pair(const Int8MatmulArgs& a, cudaStream_t stream);
 
 cudaError_t launch_append_shared(const int32_t* ids, const float* w, const float* shared_w,
                                  int32_t* ids_out, float* w_out, uint32_t num_tokens,
@@ -184,6 +190,14 @@ cudaError_t launch_zero_cols(uint8_t* dst, uint64_t rows, uint64_t pitch, uint64
 // Raise a kernel's dynamic shared-memory limit once per (kernel, device).
 cudaError_t ensure_dynamic_smem(const void* kernel, int bytes);
 
+// Streaming multiprocessors of the current device.
+inline int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2) return 148;
+  return n;
+}
+
 // Launch with programmatic stream serialization: the kernel may start while
 // the previous kernel on the stream is still running; every kernel of this
 // library calls griddep_wait() before it touches data an earlier kernel writes.
@@ -200,6 +214,27 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// The same in clusters of `cluster` CTAs along x.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, unsigned cluster,
+                               cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 

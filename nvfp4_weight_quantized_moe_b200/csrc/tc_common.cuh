@@ -8,11 +8,18 @@
 
 namespace nvm {
 
-// Device-side error word of the library (0 = no error).  Kernels set it instead
-// of trapping; the host reads it with nvfp4_moe_device_error().  Defined here:
-// this header belongs to a single translation unit (grouped_tc.cu).
+// Device-side error word (0 = no error), one per source file that includes this
+// header.  Kernels set it instead of trapping; the host reads all of them with
+// nvfp4_moe_device_error(), through each file's read_*_error function.
 enum : int { kErrNone = 0, kErrMbarTimeout = 1 };
-__device__ int g_device_error = 0;
+static __device__ int g_device_error = 0;
+// This file's word, cleared if asked.
+inline cudaError_t read_error_word(const void* symbol, int* value, bool clear) {
+  cudaError_t err = cudaMemcpyFromSymbol(value, symbol, sizeof(int));
+  if (err != cudaSuccess || !clear) return err;
+  const int zero = 0;
+  return cudaMemcpyToSymbol(symbol, &zero, sizeof(int));
+}
 
 NVM_DEV uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -104,6 +111,19 @@ NVM_DEV void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
                  "=r"(v[7])
                : "r"(taddr)
                : "memory");
+}
+
+// Each lane reads 32 consecutive 32-bit columns of its own TMEM lane.
+NVM_DEV void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -277,6 +297,37 @@ NVM_DEV void tc_mma_pair_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_des
       "r"(0u), "r"(0u)
       : "memory");
 }
+// ---------------------------------------------------------------------------
+// tcgen05.mma, kind::i8: D(tmem, s32) (+)= A(smem, s8, M x 32) * B(smem, s8, N x 32)^T,
+// both K-major; 32 k per instruction, M and N as for kind::f16.
+// ---------------------------------------------------------------------------
+__host__ __device__ constexpr uint32_t idesc_s8_s32(int m, int n) {
+  return (2u << 4)                          // D format: s32
+         | (1u << 7) | (1u << 10)           // A, B format: signed 8 bits
+         | ((uint32_t)(n >> 3) << 17)       // N / 8
+         | ((uint32_t)(m >> 4) << 24);      // M / 16
+}
+NVM_DEV void tc_mma_s8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u), "r"(0u), "r"(0u)
+      : "memory");
+}
+// The pair form: A 128 rows, B N / 2 rows from each CTA's shared memory.
+NVM_DEV void tc_mma_pair_s8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, {%5, %6, %7, %8, %9, %10, %11, %12}, p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u), "r"(0u), "r"(0u), "r"(0u), "r"(0u),
+      "r"(0u), "r"(0u)
+      : "memory");
+}
+
 // Arrive on the mbarrier at shared::cta offset `bar` in every CTA of `cta_mask`
 // once all pair MMAs this thread issued have completed.
 NVM_DEV void tc_commit_pair(uint32_t bar, uint16_t cta_mask) {
