@@ -45,21 +45,75 @@ NVM_DEV uint32_t bf16_pair(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-NVM_DEV void store_one(void* out, bool f32, uint64_t at, float v) {
-  if (f32) {
-    static_cast<float*>(out)[at] = v;
-  } else {
-    const __nv_bfloat16 b = __float2bfloat16_rn(v);
-    static_cast<uint16_t*>(out)[at] = *reinterpret_cast<const uint16_t*>(&b);
-  }
-}
-// Four consecutive outputs at an address that is a multiple of their size.
-NVM_DEV void store_four(void* out, bool f32, uint64_t at, const float (&v)[4]) {
-  if (f32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
-        make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+// The outputs of one warp's 32 token rows (lane = row, from TMEM at `taddr`) and
+// `cols` columns, written along the rows: each lane packs its row in pieces of
+// 16 bytes, which go through 4 KB of shared memory (128 bytes per row, piece p of
+// row r at p ^ (r % 8): no bank conflicts either way) so that 8 lanes write 128
+// consecutive bytes.  ws and bias are the columns' in shared memory.  Rows
+// from M on and columns from N on are not written.
+template <bool F32>
+NVM_DEV void drain_rows(uint32_t taddr, int cols, uint8_t* stage, const float* ws, const float* bias, float xs,
+                        const Int8MatmulArgs& a, uint32_t m0, uint32_t n0) {
+  constexpr int kPer = F32 ? 4 : 8;    // outputs per piece
+  constexpr int kChunk = 8 * kPer;     // columns per pass
+  const int lane = threadIdx.x & 31;
+  const uint64_t elem = F32 ? 4 : 2;
+  const bool vec = a.ldo * elem % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+#pragma unroll 1
+  for (int c0 = 0; c0 < cols && n0 + c0 < a.N; c0 += kChunk) {
+#pragma unroll
+    for (int h = 0; h < kChunk / 32; ++h) {
+      uint32_t d[32];
+      tmem_ld32(taddr + c0 + 32 * h, d);
+      tmem_wait_ld();
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 w4 = *reinterpret_cast<const float4*>(ws + c0 + 32 * h + j);
+        v[j] = scaled((int)d[j], xs, w4.x);
+        v[j + 1] = scaled((int)d[j + 1], xs, w4.y);
+        v[j + 2] = scaled((int)d[j + 2], xs, w4.z);
+        v[j + 3] = scaled((int)d[j + 3], xs, w4.w);
+      }
+      if (a.bias != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += bias[c0 + 32 * h + j];
+      }
+#pragma unroll
+      for (int p = 0; p < 32 / kPer; ++p) {
+        uint4 u;
+        if constexpr (F32)
+          u = make_uint4(__float_as_uint(v[4 * p]), __float_as_uint(v[4 * p + 1]), __float_as_uint(v[4 * p + 2]),
+                         __float_as_uint(v[4 * p + 3]));
+        else
+          u = make_uint4(bf16_pair(v[8 * p], v[8 * p + 1]), bf16_pair(v[8 * p + 2], v[8 * p + 3]),
+                         bf16_pair(v[8 * p + 4], v[8 * p + 5]), bf16_pair(v[8 * p + 6], v[8 * p + 7]));
+        const int piece = h * (32 / kPer) + p;
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((piece ^ (lane & 7)) << 4)) = u;
+      }
+    }
+    __syncwarp();
+    if (vec && n0 + c0 + kChunk <= a.N) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3), p = lane & 7;
+        const uint4 u = *reinterpret_cast<const uint4*>(stage + r * 128 + ((p ^ (r & 7)) << 4));
+        if (m0 + r < a.M)
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + ((uint64_t)(m0 + r) * a.ldo + n0 + c0 + p * kPer) * elem) = u;
+      }
+    } else {
+      // An odd row distance or the last columns: single elements, lanes along the row.
+      for (int i = lane; i < 32 * kChunk; i += 32) {
+        const int r = i / kChunk, c = i % kChunk;
+        if (m0 + r < a.M && n0 + c0 + c < a.N) {
+          const uint8_t* at = stage + r * 128 + (((c / kPer) ^ (r & 7)) << 4) + (c % kPer) * elem;
+          const uint64_t o = (uint64_t)(m0 + r) * a.ldo + n0 + c0 + c;
+          if constexpr (F32) static_cast<uint32_t*>(a.out)[o] = *reinterpret_cast<const uint32_t*>(at);
+          else static_cast<uint16_t*>(a.out)[o] = *reinterpret_cast<const uint16_t*>(at);
+        }
+      }
+    }
+    __syncwarp();
   }
 }
 
@@ -71,11 +125,7 @@ NVM_DEV int4 ld_cluster_int4(uint32_t addr) {
                : "memory");
   return v;
 }
-NVM_DEV int ld_cluster_int(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
+NVM_DEV void tmap_prefetch(const void* tmap) { asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory"); }
 
 template <int BN>
 struct TileCfg {
@@ -84,13 +134,14 @@ struct TileCfg {
   static constexpr int B_BYTES = BN * kStageK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int PITCH = BN + 4;  // ints between rows of the staged sums
-  static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
+  static constexpr int OFF_SCALE = STAGES * STAGE_BYTES;  // floats: tokens' [128], channels' [BN], biases [BN]
+  static constexpr int OFF_BAR = OFF_SCALE + 4 * (kTileM + 2 * BN);
   // full[STAGES], empty[STAGES], done
   static constexpr int NBAR = 2 * STAGES + 1;
   static constexpr int OFF_TMEM = OFF_BAR + 8 * NBAR;
   static constexpr int OFF_ABORT = OFF_TMEM + 16;
   static constexpr int SMEM = OFF_ABORT + 16 + 1024;
-  static_assert(kTileM * PITCH * 4 <= OFF_BAR, "staged sums fit the ring");
+  static_assert(kTileM * PITCH * 4 <= OFF_SCALE && 4 * 4096 <= OFF_SCALE, "staged sums and rows fit the ring");
   static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
   // Two CTAs of this size are all an SM holds, with anything that shares it: no
   // allocation of tensor memory ever waits for another cluster's.
@@ -113,13 +164,14 @@ __global__ void __launch_bounds__(kTileThreads)
   const uint32_t full = s_base + C::OFF_BAR;
   const uint32_t empty = full + 8 * C::STAGES;
   const uint32_t done = empty + 8 * C::STAGES;
+  float* scales = reinterpret_cast<float*>(smem + C::OFF_SCALE);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEM);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  griddep_wait();
-  griddep_launch_dependents();
   if (tid == 0) {
+    tmap_prefetch(&tm_x);
+    tmap_prefetch(&tm_w);
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, 1);
@@ -128,6 +180,8 @@ __global__ void __launch_bounds__(kTileThreads)
     *abort_flag = 0;
     mbar_init_fence();
   }
+  griddep_wait();
+  griddep_launch_dependents();
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), BN);
     tmem_relinquish();
@@ -189,88 +243,99 @@ __global__ void __launch_bounds__(kTileThreads)
     }
     __syncwarp();
   } else {
-    wait(done, 0);
+    const int q = warp & 3, row = 32 * q + lane;
+    const int et = tid - 64;  // 0 .. 127
+    scales[et] = m0 + et < a.M ? __ldg(a.x_scale + m0 + et) : 0.0f;
+    for (int c = et; c < BN; c += 128) {
+      scales[kTileM + c] = n0 + c < a.N ? __ldg(a.w_scale + n0 + c) : 0.0f;
+      scales[kTileM + BN + c] = a.bias != nullptr && n0 + c < a.N ? __ldg(a.bias + n0 + c) : 0.0f;
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");  // the four warps
+    const bool ok = wait(done, 0);
     __syncwarp();
     tc_fence_after();
-    // This CTA's sums into the ring's memory (every load has been consumed).
-    const int q = warp & 3, row = 32 * q + lane;
-    int* stage = reinterpret_cast<int*>(smem) + row * C::PITCH;
+    const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16);
+    if (split == 1) {
+      // Every load has been consumed: the ring's memory stages the rows.
+      if (__all_sync(0xffffffffu, ok)) {
+        uint8_t* stage = smem + q * 4096;
+        const float xs = scales[row];
+        if (a.out_f32)
+          drain_rows<true>(taddr, BN, stage, scales + kTileM, scales + kTileM + BN, xs, a, m0 + 32 * q, n0);
+        else
+          drain_rows<false>(taddr, BN, stage, scales + kTileM, scales + kTileM + BN, xs, a, m0 + 32 * q, n0);
+      }
+    } else {
+      // This CTA's sums, for its cluster.
+      int* stage = reinterpret_cast<int*>(smem) + row * C::PITCH;
 #pragma unroll 1
-    for (int c0 = 0; c0 < BN; c0 += 32) {
-      uint32_t d[32];
-      tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + c0, d);
-      tmem_wait_ld();
+      for (int c0 = 0; c0 < BN; c0 += 32) {
+        uint32_t d[32];
+        tmem_ld32(taddr + c0, d);
+        tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 32; j += 4)
-        *reinterpret_cast<int4*>(stage + c0 + j) = make_int4((int)d[j], (int)d[j + 1], (int)d[j + 2], (int)d[j + 3]);
+        for (int j = 0; j < 32; j += 4)
+          *reinterpret_cast<int4*>(stage + c0 + j) = make_int4((int)d[j], (int)d[j + 1], (int)d[j + 2], (int)d[j + 3]);
+      }
     }
     tc_fence_before();
   }
   __syncthreads();
-  if (split > 1) cluster_sync();
   if (warp == 1) tmem_dealloc(tmem, BN);
+  if (split == 1) return;
+  cluster_sync();
 
-  // Rows row_lo .. of the tile: the sums of all CTAs of the cluster, scaled.
+  // Rows 128 rank / split .. of the tile: the sums of all CTAs of the cluster, scaled.
   const int rows = kTileM / (int)split;
   const int row_lo = (int)rank * rows;
   const bool vec = a.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (a.out_f32 ? 16 : 8) == 0;
-  if (vec) {
-    for (int i = tid; i < rows * (BN / 4); i += kTileThreads) {
-      const int r = row_lo + i / (BN / 4), c = i % (BN / 4) * 4;
-      const uint32_t m = m0 + r, n = n0 + c;
-      if (m >= a.M || n >= a.N) continue;
-      const uint32_t at = s_base + (uint32_t)(r * C::PITCH + c) * 4;
-      int4 s = make_int4(0, 0, 0, 0);
-      if (split == 1) {
-        s = *reinterpret_cast<const int4*>(smem + (at - s_base));
-      } else {
-        for (uint32_t p = 0; p < split; ++p) {
-          const int4 v = ld_cluster_int4(mapa_shared(at, p));
-          s.x += v.x;
-          s.y += v.y;
-          s.z += v.z;
-          s.w += v.w;
-        }
-      }
-      const float xs = __ldg(a.x_scale + m);
-      const int sums[4] = {s.x, s.y, s.z, s.w};
-      float v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = 0.0f;
-        if (n + j < a.N) {
-          v[j] = scaled(sums[j], xs, __ldg(a.w_scale + n + j));
-          if (a.bias != nullptr) v[j] += __ldg(a.bias + n + j);
-        }
-      }
-      const uint64_t o = (uint64_t)m * a.ldo + n;
-      if (n + 4 <= a.N) {
-        store_four(a.out, a.out_f32, o, v);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (n + j < a.N) store_one(a.out, a.out_f32, o + j, v[j]);
-      }
+#pragma unroll 2
+  for (int i = tid; i < rows * (BN / 4); i += kTileThreads) {
+    const int r = row_lo + i / (BN / 4), c = i % (BN / 4) * 4;
+    const uint32_t m = m0 + r, n = n0 + c;
+    if (m >= a.M || n >= a.N) continue;
+    const uint32_t at = s_base + (uint32_t)(r * C::PITCH + c) * 4;
+    int4 s = make_int4(0, 0, 0, 0);
+    for (uint32_t p = 0; p < split; ++p) {
+      const int4 v = ld_cluster_int4(mapa_shared(at, p));
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
     }
-  } else {
-    for (int i = tid; i < rows * BN; i += kTileThreads) {
-      const int r = row_lo + i / BN, c = i % BN;
-      const uint32_t m = m0 + r, n = n0 + c;
-      if (m >= a.M || n >= a.N) continue;
-      const uint32_t at = s_base + (uint32_t)(r * C::PITCH + c) * 4;
-      int s = 0;
-      if (split == 1) {
-        s = *reinterpret_cast<const int*>(smem + (at - s_base));
+    const float xs = scales[r];
+    const float4 ws = *reinterpret_cast<const float4*>(scales + kTileM + c);
+    float4 v = make_float4(scaled(s.x, xs, ws.x), scaled(s.y, xs, ws.y), scaled(s.z, xs, ws.z), scaled(s.w, xs, ws.w));
+    if (a.bias != nullptr) {
+      const float4 b = *reinterpret_cast<const float4*>(scales + kTileM + BN + c);
+      v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+    }
+    const uint64_t o = (uint64_t)m * a.ldo + n;
+    if (a.out_f32) {
+      float* out = static_cast<float*>(a.out) + o;
+      if (vec && n + 4 <= a.N) {
+        *reinterpret_cast<float4*>(out) = v;
       } else {
-        for (uint32_t p = 0; p < split; ++p) s += ld_cluster_int(mapa_shared(at, p));
+        out[0] = v.x;
+        if (n + 1 < a.N) out[1] = v.y;
+        if (n + 2 < a.N) out[2] = v.z;
+        if (n + 3 < a.N) out[3] = v.w;
       }
-      float v = scaled(s, __ldg(a.x_scale + m), __ldg(a.w_scale + n));
-      if (a.bias != nullptr) v += __ldg(a.bias + n);
-      store_one(a.out, a.out_f32, (uint64_t)m * a.ldo + n, v);
+    } else {
+      uint16_t* out = static_cast<uint16_t*>(a.out) + o;
+      const uint32_t lo = bf16_pair(v.x, v.y), hi = bf16_pair(v.z, v.w);
+      if (vec && n + 4 <= a.N) {
+        *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+      } else {
+        out[0] = (uint16_t)lo;
+        if (n + 1 < a.N) out[1] = (uint16_t)(lo >> 16);
+        if (n + 2 < a.N) out[2] = (uint16_t)hi;
+        if (n + 3 < a.N) out[3] = (uint16_t)(hi >> 16);
+      }
     }
   }
   // A CTA's sums stay until every CTA of its cluster has read them.
-  if (split > 1) cluster_sync();
+  cluster_sync();
 }
 
 namespace {
@@ -303,12 +368,13 @@ constexpr int kPairThreads = 32 * 10;
 constexpr int kPairEpiWarps = 8;
 
 struct PairCfg8 {
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = 5;
   static constexpr int A_BYTES = kPairM / 2 * kStageK;  // this CTA's token rows
   static constexpr int B_BYTES = kPairN / 2 * kStageK;  // this CTA's half of the channels
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int OFF_SCALE = STAGES * STAGE_BYTES;  // per epilogue warp: 32 scales, 32 biases
-  static constexpr int OFF_BAR = OFF_SCALE + kPairEpiWarps * 256;
+  static constexpr int OFF_ROWS = STAGES * STAGE_BYTES;              // per epilogue warp: staged rows
+  static constexpr int OFF_SCALE = OFF_ROWS + kPairEpiWarps * 4096;  // and 128 scales, 128 biases
+  static constexpr int OFF_BAR = OFF_SCALE + kPairEpiWarps * 1024;
   // full[STAGES] (first CTA), empty[STAGES], done[2], dfree[2] (first CTA)
   static constexpr int NBAR = 2 * STAGES + 4;
   static constexpr int OFF_TMEM = OFF_BAR + 8 * NBAR;
@@ -337,9 +403,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
 
-  griddep_wait();
-  griddep_launch_dependents();
   if (tid == 0) {
+    tmap_prefetch(&tm_x);
+    tmap_prefetch(&tm_w);
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, 1);
@@ -351,6 +417,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     *abort_flag = 0;
     mbar_init_fence();
   }
+  griddep_wait();
+  griddep_launch_dependents();
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_holder), 512);
     tmem_relinquish_pair();
@@ -429,56 +497,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lane_off = (uint32_t)(32 * q) << 16;
     const uint32_t lead_dfree = mapa_shared(dfree, 0);
-    float* scale = reinterpret_cast<float*>(smem + C::OFF_SCALE) + (warp - 2) * 64;
-    const uint64_t elem = a.out_f32 ? 4 : 2;
-    const bool vec = a.ldo * elem % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+    float* scale = reinterpret_cast<float*>(smem + C::OFF_SCALE) + (warp - 2) * 256;
+    uint8_t* stage = smem + C::OFF_ROWS + (warp - 2) * 4096;
     uint32_t n = 0;
     for (uint32_t t = pair; t < ntile; t += npairs, ++n) {
       const uint32_t db = n & 1;
-      const uint32_t m = t % tiles_m * kPairM + rank * (kPairM / 2) + 32 * q + lane;
-      const uint32_t n_lo = t / tiles_m * kPairN + half * (kPairN / 2);
-      const float xs = m < a.M ? __ldg(a.x_scale + m) : 0.0f;
+      const uint32_t m0 = t % tiles_m * kPairM + rank * (kPairM / 2) + 32 * q;
+      const uint32_t n0 = t / tiles_m * kPairN + half * (kPairN / 2);
+      // This tile's scales, while its products run.
+      const float xs = m0 + lane < a.M ? __ldg(a.x_scale + m0 + lane) : 0.0f;
+#pragma unroll
+      for (int c = lane; c < kPairN / 2; c += 32) {
+        scale[c] = n0 + c < a.N ? __ldg(a.w_scale + n0 + c) : 0.0f;
+        scale[128 + c] = a.bias != nullptr && n0 + c < a.N ? __ldg(a.bias + n0 + c) : 0.0f;
+      }
+      __syncwarp();
       bool ok = wait(done + 8 * db, (n / 2) & 1);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const uint32_t dcol = tmem + lane_off + db * kPairN + half * (kPairN / 2);
-#pragma unroll 1
-      for (int c0 = 0; c0 < kPairN / 2; c0 += 32) {
-        const uint32_t n0 = n_lo + c0;
-        if (n0 >= a.N) break;
-        __syncwarp();
-        scale[lane] = n0 + lane < a.N ? __ldg(a.w_scale + n0 + lane) : 0.0f;
-        scale[32 + lane] = a.bias != nullptr && n0 + lane < a.N ? __ldg(a.bias + n0 + lane) : 0.0f;
-        __syncwarp();
-        uint32_t d[32];
-        tmem_ld32(dcol + c0, d);
-        tmem_wait_ld();
-        if (!ok || m >= a.M) continue;
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = scaled((int)d[j], xs, scale[j]);
-        if (a.bias != nullptr) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] += scale[32 + j];
-        }
-        const uint64_t o = (uint64_t)m * a.ldo + n0;
-        if (vec && n0 + 32 <= a.N) {
-          if (a.out_f32) {
-            float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-          } else {
-            uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + o);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              p[j] = make_uint4(bf16_pair(v[8 * j], v[8 * j + 1]), bf16_pair(v[8 * j + 2], v[8 * j + 3]),
-                                bf16_pair(v[8 * j + 4], v[8 * j + 5]), bf16_pair(v[8 * j + 6], v[8 * j + 7]));
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (n0 + j < a.N) store_one(a.out, a.out_f32, o + j, v[j]);
-        }
+      if (ok && m0 < a.M) {
+        if (a.out_f32) drain_rows<true>(dcol, kPairN / 2, stage, scale, scale + 128, xs, a, m0, n0);
+        else drain_rows<false>(dcol, kPairN / 2, stage, scale, scale + 128, xs, a, m0, n0);
       }
       tc_fence_before();
       __syncwarp();
