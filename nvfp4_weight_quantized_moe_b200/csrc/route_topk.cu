@@ -8,16 +8,19 @@
 //
 // Every comparison goes by the exact values, ties to the lower index.  Without
 // a bias the choice is made on the logits themselves (s is monotone in l), which
-// is exact.  With a bias, or with sums of two scores, c is computed in FP32 and
-// neighbours in the order that are closer than its error bound send the row
-// through the same selection in FP64 (a few rows in a thousand): FP32 alone
-// would order about one row in 5000 of a 256-expert router differently.
+// is exact.  With a bias, or with sums of two scores, c is computed in FP32, and
+// a row in which two values whose order matters are closer than the error bound
+// goes through the same selection once more in FP64: about one row in 1000 of a
+// 256-expert router, where FP32 alone would order one in 5000 differently.
 //
-// One warp per token: lane i holds experts i, i + 32, ...; maxima and minima are
-// single redux instructions on order-preserving integer keys; lane s holds
-// choice s, so topk <= 32 and num_groups <= 32.  The work is one read of the
-// logits; per token it is a chain of topk dependent warp reductions, hidden by
-// the other warps of the SM for large batches.
+// One warp per token.  Lane i holds ceil(E / 32) consecutive experts, so a
+// lower lane means a lower index, a tie is settled by the lowest set bit of a
+// ballot, and where a group is whole lanes the best two of all groups are found
+// at once by a butterfly inside the group's lanes.  Maxima are single redux
+// instructions on order-preserving integer keys.  Lane s ends up with choice s,
+// so topk <= 32 and num_groups <= 32.  The work is one read of the logits; per
+// token it is a chain of topk dependent warp reductions, hidden by the other
+// warps of the SM for large batches.
 
 #include <cfloat>
 #include <climits>
@@ -78,6 +81,8 @@ NVM_DEV F warp_sum(F v) {
   return v;
 }
 
+constexpr int kMaxWarps = 8;
+
 struct RouteArgs {
   const void* logits;
   const float* bias;
@@ -85,172 +90,173 @@ struct RouteArgs {
   float* weights;
   uint64_t ld;
   uint32_t M;
-  int E, topk, groups, topk_groups, group_top, group_size;
+  int E, per_lane;  // per_lane = ceil(E / 32)
+  int topk, groups, topk_groups, group_top;
+  int group_lanes;       // lanes of a group, if groups are whole lanes; else 0
+  uint32_t group_magic;  // ceil(2^20 / group size): expert e is in group e * magic >> 20
   int softmax, renorm;
+  int vec;               // rows can be read 16 bytes (bf16 of 128 experts: 8) at a time
   float scale;
 };
 
-// The chosen experts of one row: lane s gets choice s (id, or -1) and its logit.
-struct Choice {
-  int id;
-  float logit;
-};
+// exp for scores that are only compared (FP32: the hardware exponential) ...
+NVM_DEV float exp_near(float v) { return __expf(v); }
+NVM_DEV double exp_near(double v) { return exp(v); }
+NVM_DEV float recip_near(float v) { return __fdividef(1.0f, v); }
+NVM_DEV double recip_near(double v) { return 1.0 / v; }
 
-// The selection in the arithmetic of F.  l[j] is the logit of expert 32 j + lane
-// (-infinity: not choosable), lmax and zinv the softmax's maximum and 1 / sum.
-// `near` reports that two values whose order matters lie within the FP32 error
-// bound of each other; F = double never reports it.
+// The selection in the arithmetic of F: the chosen experts, best first, into
+// picks[0 .. topk) (-1 where none is left).  l[j] is the logit of expert
+// per_lane * lane + j (-infinity: not choosable), lmax and zinv the softmax's
+// maximum and 1 / sum.  Returns whether two values whose order matters lie within
+// the FP32 error bound of each other (never for F = double).
 template <typename F, int EPL>
-NVM_DEV Choice select_experts(const RouteArgs& a, const float (&l)[EPL], F lmax, F zinv, bool& near) {
+NVM_DEV bool select_experts(const RouteArgs& a, const float (&l)[EPL], F lmax, F zinv, int* picks) {
   using Key = typename KeyOf<F>::type;
-  const int lane = threadIdx.x & 31;
-  const bool scored = a.bias != nullptr;          // the choice is s + bias; else the logit
-  const bool group_scored = scored || a.group_top > 1;
-  // FP32 error of s: at most 2^-19 of the largest score (exp and the quotient a
-  // few 2^-24 each, a sum of at most 32 terms per lane and 5 tree steps, the
-  // rounding of l - lmax weighed by exp(l - lmax)), for softmax 1 / sum at most
-  // and 1 for sigmoid; of the sum s + bias: 2^-24 of its value.  The bound
-  // compared with covers the errors of both neighbours.
-  const float smax = a.softmax ? (float)zinv : 1.0f;
-  auto bound = [&](float v) { return smax * 0x1p-18f + fabsf(v) * 0x1p-22f; };
+  constexpr bool kFast = sizeof(F) == 4;
+  constexpr int kUnroll = kFast ? EPL : 1;  // FP64 is rare: small code, few registers
+  const int lane = threadIdx.x & 31, e0 = lane * a.per_lane;
+  const bool scored = a.bias != nullptr;  // the choice is s + bias; else the logit
+  // Error of an FP32 s.  Sigmoid: the exponential is off by (2 + 1.2 |x|) 2^-23 of
+  // its value, which s (1 - s) weighs to under 2^-23; 1 + exp and the quotient add
+  // 2^-24 and 2^-22: under 2^-21.  Softmax, in units of the largest score 1 / sum:
+  // the difference and the exponential as much, the sum EPL + 5 roundings.  s + bias
+  // adds 2^-24 of its value.  Twice that for two neighbours.
+  const float unit = a.softmax ? (float)zinv * (8 + 2 * (EPL + 5)) * 0x1p-23f : 0x1p-20f;
+  auto bound = [&](float v) { return unit + fabsf(v) * 0x1p-23f; };
   auto score = [&](float x) -> F {
-    if (a.softmax) return exp_f((F)x - lmax) * zinv;
-    return (F)1 / ((F)1 + exp_f(-(F)x));
+    if (a.softmax) return exp_near((F)x - lmax) * zinv;
+    return recip_near((F)1 + exp_near(-(F)x));
   };
 
   Key key[EPL];
-  float b[EPL];
-#pragma unroll
+#pragma unroll kUnroll
   for (int j = 0; j < EPL; ++j) {
-    const int e = 32 * j + lane;
     key[j] = 0;
-    b[j] = 0.0f;
     if (l[j] == -INFINITY) continue;
-    if (scored) {
-      b[j] = __ldg(a.bias + e);
-      const F c = score(l[j]) + (F)b[j];
-      if (c > -(F)INFINITY) key[j] = order_key(c);  // false for NaN too
-    } else {
-      key[j] = order_key((F)l[j]);
-    }
+    F c = (F)l[j];
+    if (scored) c = score(l[j]) + (F)__ldg(a.bias + e0 + j);
+    if (c > -(F)INFINITY) key[j] = order_key(c);  // false for NaN too
   }
 
+  bool near = false;
   if (a.groups > 1) {
-    // Lane g gets the score of group g: its best value, or the sum of the best
-    // two (of the one, where only one can be chosen).
-    F mine = -(F)INFINITY;
-    bool some = false;
-    for (int g = 0; g < a.groups; ++g) {
-      const int lo = g * a.group_size, hi = lo + a.group_size;
-      Key k1 = 0, k2 = 0;  // this lane's best two
-#pragma unroll
+    // Lane g gets the score of group g: its best value, or the sum of its best two
+    // (of the one, where only one can be chosen); key 0: no expert to choose.
+    const bool sums = a.group_top > 1;
+    auto value_key = [&](int j) -> Key {
+      return key[j] == 0 || scored || !sums ? key[j] : order_key(score(l[j]));
+    };
+    auto total = [&](Key k1, Key k2) -> Key {
+      if (k1 == 0 || k2 == 0 || !sums) return k1;
+      return order_key(key_value(k1, F()) + key_value(k2, F()));
+    };
+    Key mine = 0;
+    if (a.group_lanes > 0) {
+      Key k1 = 0, k2 = 0;
+#pragma unroll kUnroll
       for (int j = 0; j < EPL; ++j) {
-        const int e = 32 * j + lane;
-        Key k = 0;
-        if (e >= lo && e < hi && key[j] != 0) k = scored || !group_scored ? key[j] : order_key(score(l[j]));
-        const Key lower = k < k1 ? k : k1;
+        const Key k = value_key(j), lower = k < k1 ? k : k1;
         k1 = k > k1 ? k : k1;
         k2 = lower > k2 ? lower : k2;
       }
-      const Key best = warp_max_key(k1);
-      F v = best != 0 ? key_value(best, F()) : -(F)INFINITY;
-      if (a.group_top > 1 && best != 0) {
+      for (int o = 1; o < a.group_lanes; o <<= 1) {
+        const Key p1 = __shfl_xor_sync(kFull, k1, o), p2 = __shfl_xor_sync(kFull, k2, o);
+        const Key lower = p1 < k1 ? p1 : k1, second = p2 > k2 ? p2 : k2;
+        k1 = p1 > k1 ? p1 : k1;
+        k2 = lower > second ? lower : second;
+      }
+      mine = __shfl_sync(kFull, total(k1, k2), lane * a.group_lanes & 31);
+      if (lane >= a.groups) mine = 0;
+    } else {
+#pragma unroll 1
+      for (int g = 0; g < a.groups; ++g) {
+        Key k1 = 0, k2 = 0;  // this lane's best two
+#pragma unroll kUnroll
+        for (int j = 0; j < EPL; ++j) {
+          if (key[j] == 0 || (int)((uint32_t)(e0 + j) * a.group_magic >> 20) != g) continue;
+          const Key k = value_key(j), lower = k < k1 ? k : k1;
+          k1 = k > k1 ? k : k1;
+          k2 = lower > k2 ? lower : k2;
+        }
+        const Key best = warp_max_key(k1);
         const unsigned at = __ballot_sync(kFull, k1 == best);
         const Key next = warp_max_key(lane == __ffs(at) - 1 ? k2 : k1);
-        if (next != 0) v += key_value(next, F());
-      }
-      if (lane == g) {
-        mine = v;
-        some = best != 0;
+        if (lane == g) mine = total(best, next);
       }
     }
-    // Rank of this lane's group; a group's rank counts the better ones.
+    // A group's rank counts the better ones.
     int rank = 0;
-    F above = (F)INFINITY, below = -(F)INFINITY;  // nearest neighbours across the border
-    const bool kept_before = some;
+#pragma unroll 1
     for (int g = 0; g < a.groups; ++g) {
-      const F v = __shfl_sync(kFull, mine, g);
-      const bool there = __shfl_sync(kFull, (int)some, g) != 0;
-      if (there && (v > mine || (v == mine && g < lane))) ++rank;
+      const Key v = __shfl_sync(kFull, mine, g);
+      rank += v > mine || (v == mine && g < lane);
     }
-    const bool kept = kept_before && rank < a.topk_groups;
+    const bool kept = mine != 0 && rank < a.topk_groups;
     const unsigned kept_mask = __ballot_sync(kFull, kept);
-    if (sizeof(F) == 4 && group_scored) {
-      // The worst kept against the best left out.
-      above = kept ? mine : (F)INFINITY;
-      below = some && !kept ? mine : -(F)INFINITY;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const F x = __shfl_xor_sync(kFull, above, o), y = __shfl_xor_sync(kFull, below, o);
-        above = x < above ? x : above;
-        below = y > below ? y : below;
+    if constexpr (kFast) {
+      // The worst kept against the best left out (there may be none).
+      const Key above = __reduce_min_sync(kFull, kept ? mine : 0xffffffffu);
+      const Key below = __reduce_max_sync(kFull, kept ? 0u : mine);
+      if ((scored || sums) && below != 0) {
+        const float v = key_value(above, F());
+        near = v - key_value(below, F()) <= a.group_top * bound(v);
       }
-      if (above - below <= (F)(a.group_top * bound((float)above))) near = true;
     }
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (key[j] != 0 && ((kept_mask >> ((32 * j + lane) / a.group_size)) & 1u) == 0) key[j] = 0;
+    if (a.group_lanes > 0) {
+      if (((kept_mask >> (lane / a.group_lanes)) & 1u) == 0) {
+#pragma unroll kUnroll
+        for (int j = 0; j < EPL; ++j) key[j] = 0;
+      }
+    } else {
+#pragma unroll kUnroll
+      for (int j = 0; j < EPL; ++j)
+        if (key[j] != 0 && ((kept_mask >> ((uint32_t)(e0 + j) * a.group_magic >> 20)) & 1u) == 0) key[j] = 0;
+    }
   }
 
-  // topk times: the best key, ties to the lowest expert.  A lane keeps the best
-  // of its own experts; the lane whose expert was taken looks again.
-  Choice mine{-1, 0.0f};
+  // topk times the best key of the warp.  A lane keeps the best of its own experts;
+  // the lane whose expert was taken looks again.  One more round, where
+  // neighbours are watched, for the best left out.
+  if (lane < a.topk) picks[lane] = -1;
+  __syncwarp();
+  const bool watch = kFast && scored;
+  const int rounds = watch ? a.topk + 1 : a.topk;
   Key best = 0;
-  int best_e = INT_MAX;
-  float best_l = 0.0f, best_b = 0.0f;
-  auto look = [&]() {
-    best = 0;
-    best_e = INT_MAX;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (key[j] > best) {
-        best = key[j];
-        best_e = 32 * j + lane;
-        best_l = l[j];
-        best_b = b[j];
-      }
-  };
-  look();
-  const bool watch = sizeof(F) == 4 && scored;
-  const int picks = watch ? a.topk + 1 : a.topk;  // one more: the best left out
-  float last = 0.0f, last_l = 0.0f, last_b = 0.0f;
-  for (int s = 0; s < picks; ++s) {
+  int best_j = 0;
+#pragma unroll kUnroll
+  for (int j = 0; j < EPL; ++j)
+    if (key[j] > best) {
+      best = key[j];
+      best_j = j;
+    }
+  float last = INFINITY;
+#pragma unroll 1
+  for (int s = 0; s < rounds; ++s) {
     const Key top = warp_max_key(best);
     if (top == 0) break;
-    const int e = __reduce_min_sync(kFull, best == top ? best_e : INT_MAX);
-    const float el = __shfl_sync(kFull, best_l, e & 31);
     if (watch) {
-      const float eb = __shfl_sync(kFull, best_b, e & 31);
       const float v = (float)key_value(top, F());
-      // Equal logits and biases are equal in any arithmetic.
-      if (s > 0 && last - v <= bound(last) && !(el == last_l && eb == last_b)) near = true;
+      near |= last - v <= bound(v);  // infinity - infinity is no near pair
       last = v;
-      last_l = el;
-      last_b = eb;
     }
-    if (s < a.topk && lane == s) mine = Choice{e, el};
-    if (best_e == e) {
-#pragma unroll
-      for (int j = 0; j < EPL; ++j)
-        if (32 * j + lane == e) key[j] = 0;
-      look();
+    const unsigned at = __ballot_sync(kFull, best == top);
+    if (lane == __ffs(at) - 1) {
+      if (s < a.topk) picks[s] = e0 + best_j;
+      best = 0;
+      const int taken = best_j;
+#pragma unroll kUnroll
+      for (int j = 0; j < EPL; ++j) {
+        if (j == taken) key[j] = 0;
+        if (key[j] > best) {
+          best = key[j];
+          best_j = j;
+        }
+      }
     }
   }
-  return mine;
-}
-
-// The FP64 form, out of line: rows whose FP32 order is not certain.
-template <int EPL>
-__device__ __noinline__ Choice select_exactly(const RouteArgs& a, const float (&l)[EPL], float lmax) {
-  double zinv = 0.0;
-  if (a.softmax) {
-    double z = 0.0;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) z += exp((double)l[j] - (double)lmax);
-    zinv = 1.0 / warp_sum(z);
-  }
-  bool near = false;
-  return select_experts<double, EPL>(a, l, (double)lmax, zinv, near);
+  __syncwarp();
+  return near;
 }
 
 template <typename T>
@@ -264,81 +270,101 @@ NVM_DEV float logit_f32(uint16_t v) {
   return bf16_bits_to_f32(v);
 }
 
+// A NaN logit counts as -infinity (not choosable), +infinity as the largest
+// finite value.
+NVM_DEV float clean_logit(float v) { return v != v ? -INFINITY : fminf(v, FLT_MAX); }
+
+template <typename T, int EPL>
+NVM_DEV void load_logits(const RouteArgs& a, const T* row, float (&l)[EPL]) {
+  constexpr int kPer = 16 / sizeof(T) < EPL ? 16 / sizeof(T) : EPL;  // elements of one load
+  const int e0 = (threadIdx.x & 31) * a.per_lane;
+  if (a.vec) {  // per_lane == EPL, E == 32 EPL
+    struct alignas(kPer * sizeof(T)) Piece {
+      T v[kPer];
+    };
+    Piece p[EPL / kPer];
+#pragma unroll
+    for (int i = 0; i < EPL / kPer; ++i) p[i] = reinterpret_cast<const Piece*>(row + e0)[i];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) l[j] = clean_logit(logit_f32<T>(p[j / kPer].v[j % kPer]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      l[j] = -INFINITY;
+      if (j < a.per_lane && e0 + j < a.E) l[j] = clean_logit(logit_f32<T>(__ldg(row + e0 + j)));
+    }
+  }
+}
+
+// The FP64 selection of a row whose FP32 order is not certain, out of line; it
+// reads the row again, so nothing has to be kept for it.
+template <typename T, int EPL>
+__device__ __noinline__ void select_exactly(const RouteArgs& a, const T* row, float lmax, int* picks) {
+  float l[EPL];
+  load_logits<T, EPL>(a, row, l);
+  double zinv = 0.0;
+  if (a.softmax) {
+    double z = 0.0;
+    for (int j = 0; j < EPL; ++j) z += exp((double)l[j] - (double)lmax);
+    zinv = 1.0 / warp_sum(z);
+  }
+  select_experts<double, EPL>(a, l, (double)lmax, zinv, picks);
+}
+
 }  // namespace
 
 template <typename T, int EPL>
-__global__ void __launch_bounds__(256) route_topk_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(32 * kMaxWarps, EPL <= 8 ? 4 : EPL == 16 ? 2 : 1) route_topk_kernel(const RouteArgs a) {
+  __shared__ int s_picks[kMaxWarps][32];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const uint32_t t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= a.M) return;
   const T* row = static_cast<const T*>(a.logits) + (uint64_t)t * a.ld;
+  int* picks = s_picks[threadIdx.x >> 5];
 
-  // A NaN logit counts as -infinity (not choosable), +infinity as the largest
-  // finite value.
   float l[EPL];
-  T raw[EPL];
+  load_logits<T, EPL>(a, row, l);
+  // Softmax's maximum, and 1 / sum where the scores as such are needed: not for
+  // renormalised weights or a choice by logits.
+  float lmax = 0.0f, zinv = 0.0f;
+  if (a.softmax) {
+    lmax = l[0];
 #pragma unroll
-  for (int j = 0; j < EPL; ++j)
-    if (32 * j + lane < a.E) raw[j] = __ldg(row + 32 * j + lane);
-  float lmax = -INFINITY;
+    for (int j = 1; j < EPL; ++j) lmax = fmaxf(lmax, l[j]);
+    lmax = key_value(__reduce_max_sync(kFull, order_key(lmax)), 0.0f);
+    if (lmax != -INFINITY && (a.bias != nullptr || a.group_top > 1 || !a.renorm)) {
+      float z = 0.0f;
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    float v = -INFINITY;
-    if (32 * j + lane < a.E) v = logit_f32<T>(raw[j]);
-    l[j] = v != v ? -INFINITY : fminf(v, FLT_MAX);
-    lmax = fmaxf(lmax, l[j]);
+      for (int j = 0; j < EPL; ++j) z += expf(l[j] - lmax);
+      zinv = 1.0f / warp_sum(z);
+    }
   }
-  lmax = warp_max(lmax);
-
-  // Softmax's 1 / sum: needed for the scores as such, not for renormalised
-  // weights or a choice by logits.
-  const bool scored = a.bias != nullptr || (a.groups > 1 && a.group_top > 1);
-  float zinv = 0.0f;
-  if (a.softmax && (scored || !a.renorm) && lmax != -INFINITY) {
-    float z = 0.0f;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) z += expf(l[j] - lmax);
-    zinv = 1.0f / warp_sum(z);
-  }
-
-  bool near = false;
-  Choice c = select_experts<float, EPL>(a, l, lmax, zinv, near);
-  if (near) c = select_exactly<EPL>(a, l, lmax);
+  if (select_experts<float, EPL>(a, l, lmax, zinv, picks)) select_exactly<T, EPL>(a, row, lmax, picks);
 
   // Weights.  Renormalised ones are formed relative to the largest chosen
   // logit, so they are never 0 / 0: softmax exp(l - top); sigmoid
   // exp(l - base) / (1 + exp(l)) with base = min(0, top).
-  const bool there = c.id >= 0;
-  float w = 0.0f;
+  const int id = lane < a.topk ? picks[lane] : -1;
+  const float x = id >= 0 ? clean_logit(logit_f32<T>(__ldg(row + id))) : -INFINITY;
+  float base = a.softmax ? lmax : 0.0f;
   if (a.renorm) {
-    const float top = warp_max(there ? c.logit : -INFINITY);
-    if (there) {
-      if (a.softmax) {
-        w = expf(c.logit - top);
-      } else if (c.logit > 0.0f) {
-        w = 1.0f / (1.0f + expf(-c.logit));
-      } else {
-        w = expf(c.logit - fminf(0.0f, top)) / (1.0f + expf(c.logit));
-      }
-    }
-    const float sum = warp_sum(w);
-    if (there) w = w / sum;
-  } else if (there) {
-    if (a.softmax) {
-      w = expf(c.logit - lmax) * zinv;
-    } else if (c.logit > 0.0f) {
-      w = 1.0f / (1.0f + expf(-c.logit));
-    } else {
-      const float x = expf(c.logit);
-      w = x / (1.0f + x);
-    }
+    base = key_value(__reduce_max_sync(kFull, order_key(x)), 0.0f);
+    if (!a.softmax) base = fminf(base, 0.0f);
   }
+  float w = 0.0f;
+  if (id >= 0) {
+    const float low = expf(fminf(x, a.softmax ? x : 0.0f) - base);
+    w = low;
+    if (!a.softmax) w = x > 0.0f ? 1.0f / (1.0f + expf(-x)) : low / (1.0f + expf(x));
+  }
+  float norm = a.softmax ? zinv : 1.0f;
+  if (a.renorm) norm = 1.0f / warp_sum(w);
   if (lane < a.topk) {
     const uint64_t at = (uint64_t)t * a.topk + lane;
-    a.ids[at] = c.id;
-    a.weights[at] = w * a.scale;
+    a.ids[at] = id;
+    a.weights[at] = id >= 0 ? w * norm * a.scale : 0.0f;
   }
 }
 
@@ -348,9 +374,9 @@ template <typename T>
 cudaError_t launch_route_topk_of(const RouteArgs& a, cudaStream_t stream) {
   // One warp per CTA while that leaves every SM at most a few tokens (their
   // chains then run on separate schedulers), eight for large batches.
-  const int warps = a.M <= 592 ? 1 : 8;
+  const int warps = a.M <= 592 ? 1 : kMaxWarps;
   const dim3 grid((a.M + warps - 1) / warps), block(32 * warps);
-  const int epl = (a.E + 31) / 32;
+  const int epl = a.per_lane;
   if (epl <= 1) return launch_pdl(route_topk_kernel<T, 1>, grid, block, 0, stream, a);
   if (epl <= 2) return launch_pdl(route_topk_kernel<T, 2>, grid, block, 0, stream, a);
   if (epl <= 4) return launch_pdl(route_topk_kernel<T, 4>, grid, block, 0, stream, a);
@@ -375,7 +401,15 @@ cudaError_t launch_route_topk(const void* logits, bool logits_f32, uint64_t ld, 
   a.groups = (int)r.num_groups;
   a.topk_groups = (int)r.topk_groups;
   a.group_top = (int)r.group_top;
-  a.group_size = (int)(r.num_experts / r.num_groups);
+  const uint32_t group_size = r.num_experts / r.num_groups;
+  a.per_lane = (a.E + 31) / 32;
+  a.group_magic = ((1u << 20) + group_size - 1) / group_size;
+  if (r.num_experts % 32 == 0 && 32 % r.num_groups == 0) a.group_lanes = 32 / a.groups;
+  // Wide reads: whole lanes of a power of two of experts, on 16 bytes (or on the
+  // lane's bytes, where they are fewer).
+  const uint32_t lane_bytes = (uint32_t)a.per_lane * (logits_f32 ? 4 : 2), piece = lane_bytes < 16 ? lane_bytes : 16;
+  a.vec = r.num_experts % 32 == 0 && (a.per_lane & (a.per_lane - 1)) == 0 &&
+          reinterpret_cast<uintptr_t>(logits) % piece == 0 && ld * (logits_f32 ? 4 : 2) % piece == 0;
   a.softmax = r.softmax;
   a.renorm = r.renormalize;
   a.scale = r.scale;
