@@ -9,9 +9,9 @@
 // Every comparison goes by the exact values, ties to the lower index.  Without
 // a bias the choice is made on the logits themselves (s is monotone in l), which
 // is exact.  With a bias, or with sums of two scores, c is computed in FP32, and
-// a row in which two values whose order matters are closer than the error bound
-// goes through the same selection once more in FP64: about one row in 1000 of a
-// 256-expert router, where FP32 alone would order one in 5000 differently.
+// where two values whose order matters are closer than its error bound, they are
+// computed again in FP64: in about one row in 1000 of a 256-expert router, where
+// FP32 alone would order one in 5000 differently.
 //
 // One warp per token.  Lane i holds ceil(E / 32) consecutive experts, so a
 // lower lane means a lower index, a tie is settled by the lowest set bit of a
@@ -34,8 +34,8 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
-// Order-preserving integer keys; 0 marks an expert that cannot be chosen (every
-// finite value and +infinity has a larger key).
+// Order-preserving integer keys.  An expert can be chosen if its key is above
+// that of -infinity; 0 marks one that was taken or whose group was left out.
 NVM_DEV uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);  // -0 and +0 are the same value
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
@@ -55,11 +55,15 @@ struct KeyOf;
 template <>
 struct KeyOf<float> {
   using type = uint32_t;
+  static constexpr uint32_t none = 0x007fffffu;  // of -infinity
 };
 template <>
 struct KeyOf<double> {
   using type = uint64_t;
+  static constexpr uint64_t none = 0x000fffffffffffffull;
 };
+NVM_DEV float or_minus_infinity(float v) { return fmaxf(v, -INFINITY); }  // NaN to -infinity
+NVM_DEV double or_minus_infinity(double v) { return fmax(v, -(double)INFINITY); }
 
 NVM_DEV uint32_t warp_max_key(uint32_t k) { return __reduce_max_sync(kFull, k); }
 NVM_DEV uint64_t warp_max_key(uint64_t k) {
@@ -71,9 +75,6 @@ NVM_DEV uint64_t warp_max_key(uint64_t k) {
   return k;
 }
 
-NVM_DEV float exp_f(float v) { return expf(v); }
-NVM_DEV double exp_f(double v) { return exp(v); }
-
 template <typename F>
 NVM_DEV F warp_sum(F v) {
 #pragma unroll
@@ -81,7 +82,7 @@ NVM_DEV F warp_sum(F v) {
   return v;
 }
 
-constexpr int kMaxWarps = 8;
+constexpr int kMaxWarps = 4;
 
 struct RouteArgs {
   const void* logits;
@@ -96,167 +97,87 @@ struct RouteArgs {
   uint32_t group_magic;  // ceil(2^20 / group size): expert e is in group e * magic >> 20
   int softmax, renorm;
   int vec;               // rows can be read 16 bytes (bf16 of 128 experts: 8) at a time
+  int vec_bias;          // so can the bias
   float scale;
 };
 
-// exp for scores that are only compared (FP32: the hardware exponential) ...
-NVM_DEV float exp_near(float v) { return __expf(v); }
-NVM_DEV double exp_near(double v) { return exp(v); }
-NVM_DEV float recip_near(float v) { return __fdividef(1.0f, v); }
-NVM_DEV double recip_near(double v) { return 1.0 / v; }
+// What a warp's selection leaves in shared memory.
+struct alignas(16) Picks {
+  int id[32];           // the chosen experts, best first; -1 where none is left
+  float logit[32];      // their logits
+  uint32_t key[32];     // candidates in the order of their index: keys (0 past them), ...
+  int expert[32];       // ... experts and
+  float found[32];      // logits
+  uint2 ranked[32];     // the best of them, best first (key, expert)
+};
 
-// The selection in the arithmetic of F: the chosen experts, best first, into
-// picks[0 .. topk) (-1 where none is left).  l[j] is the logit of expert
-// per_lane * lane + j (-infinity: not choosable), lmax and zinv the softmax's
-// maximum and 1 / sum.  Returns whether two values whose order matters lie within
-// the FP32 error bound of each other (never for F = double).
-template <typename F, int EPL>
-NVM_DEV bool select_experts(const RouteArgs& a, const float (&l)[EPL], F lmax, F zinv, int* picks) {
+// The groups of a row and the lanes' experts: expert e's group, or whether it stays.
+NVM_DEV bool in_mask(const RouteArgs& a, uint32_t mask, int e) {
+  return ((mask >> ((uint32_t)e * a.group_magic >> 20)) & 1u) != 0;
+}
+
+// Lane g gets the key of the score of group g from `value`, the choice keys of the
+// lane's experts: of the best value, or of the sum of the best two (of the one,
+// where only one can be chosen).
+template <typename F, int EPL, typename Value>
+NVM_DEV typename KeyOf<F>::type group_scores(const RouteArgs& a, Value value) {
   using Key = typename KeyOf<F>::type;
-  constexpr bool kFast = sizeof(F) == 4;
-  constexpr int kUnroll = kFast ? EPL : 1;  // FP64 is rare: small code, few registers
+  constexpr int kUnroll = sizeof(F) == 4 ? EPL : 1;
+  constexpr Key kNone = KeyOf<F>::none;
   const int lane = threadIdx.x & 31, e0 = lane * a.per_lane;
-  const bool scored = a.bias != nullptr;  // the choice is s + bias; else the logit
-  // Error of an FP32 s.  Sigmoid: the exponential is off by (2 + 1.2 |x|) 2^-23 of
-  // its value, which s (1 - s) weighs to under 2^-23; 1 + exp and the quotient add
-  // 2^-24 and 2^-22: under 2^-21.  Softmax, in units of the largest score 1 / sum:
-  // the difference and the exponential as much, the sum EPL + 5 roundings.  s + bias
-  // adds 2^-24 of its value.  Twice that for two neighbours.
-  const float unit = a.softmax ? (float)zinv * (8 + 2 * (EPL + 5)) * 0x1p-23f : 0x1p-20f;
-  auto bound = [&](float v) { return unit + fabsf(v) * 0x1p-23f; };
-  auto score = [&](float x) -> F {
-    if (a.softmax) return exp_near((F)x - lmax) * zinv;
-    return recip_near((F)1 + exp_near(-(F)x));
+  auto total = [&](Key k1, Key k2) -> Key {
+    if (k1 <= kNone || k2 <= kNone || a.group_top < 2) return k1;
+    return order_key(key_value(k1, F()) + key_value(k2, F()));
   };
-
-  Key key[EPL];
+  if (a.group_lanes > 0) {
+    Key k1 = 0, k2 = 0;
 #pragma unroll kUnroll
-  for (int j = 0; j < EPL; ++j) {
-    key[j] = 0;
-    if (l[j] == -INFINITY) continue;
-    F c = (F)l[j];
-    if (scored) c = score(l[j]) + (F)__ldg(a.bias + e0 + j);
-    if (c > -(F)INFINITY) key[j] = order_key(c);  // false for NaN too
-  }
-
-  bool near = false;
-  if (a.groups > 1) {
-    // Lane g gets the score of group g: its best value, or the sum of its best two
-    // (of the one, where only one can be chosen); key 0: no expert to choose.
-    const bool sums = a.group_top > 1;
-    auto value_key = [&](int j) -> Key {
-      return key[j] == 0 || scored || !sums ? key[j] : order_key(score(l[j]));
-    };
-    auto total = [&](Key k1, Key k2) -> Key {
-      if (k1 == 0 || k2 == 0 || !sums) return k1;
-      return order_key(key_value(k1, F()) + key_value(k2, F()));
-    };
-    Key mine = 0;
-    if (a.group_lanes > 0) {
-      Key k1 = 0, k2 = 0;
-#pragma unroll kUnroll
-      for (int j = 0; j < EPL; ++j) {
-        const Key k = value_key(j), lower = k < k1 ? k : k1;
-        k1 = k > k1 ? k : k1;
-        k2 = lower > k2 ? lower : k2;
-      }
-      for (int o = 1; o < a.group_lanes; o <<= 1) {
-        const Key p1 = __shfl_xor_sync(kFull, k1, o), p2 = __shfl_xor_sync(kFull, k2, o);
-        const Key lower = p1 < k1 ? p1 : k1, second = p2 > k2 ? p2 : k2;
-        k1 = p1 > k1 ? p1 : k1;
-        k2 = lower > second ? lower : second;
-      }
-      mine = __shfl_sync(kFull, total(k1, k2), lane * a.group_lanes & 31);
-      if (lane >= a.groups) mine = 0;
-    } else {
+    for (int j = 0; j < EPL; ++j) {
+      const Key k = value(j), lower = k < k1 ? k : k1;
+      k1 = k > k1 ? k : k1;
+      k2 = lower > k2 ? lower : k2;
+    }
 #pragma unroll 1
-      for (int g = 0; g < a.groups; ++g) {
-        Key k1 = 0, k2 = 0;  // this lane's best two
-#pragma unroll kUnroll
-        for (int j = 0; j < EPL; ++j) {
-          if (key[j] == 0 || (int)((uint32_t)(e0 + j) * a.group_magic >> 20) != g) continue;
-          const Key k = value_key(j), lower = k < k1 ? k : k1;
-          k1 = k > k1 ? k : k1;
-          k2 = lower > k2 ? lower : k2;
-        }
-        const Key best = warp_max_key(k1);
-        const unsigned at = __ballot_sync(kFull, k1 == best);
-        const Key next = warp_max_key(lane == __ffs(at) - 1 ? k2 : k1);
-        if (lane == g) mine = total(best, next);
-      }
+    for (int o = 1; o < a.group_lanes; o <<= 1) {
+      const Key p1 = __shfl_xor_sync(kFull, k1, o), p2 = __shfl_xor_sync(kFull, k2, o);
+      const Key lower = p1 < k1 ? p1 : k1, second = p2 > k2 ? p2 : k2;
+      k1 = p1 > k1 ? p1 : k1;
+      k2 = lower > second ? lower : second;
     }
-    // A group's rank counts the better ones.
-    int rank = 0;
-#pragma unroll 1
-    for (int g = 0; g < a.groups; ++g) {
-      const Key v = __shfl_sync(kFull, mine, g);
-      rank += v > mine || (v == mine && g < lane);
-    }
-    const bool kept = mine != 0 && rank < a.topk_groups;
-    const unsigned kept_mask = __ballot_sync(kFull, kept);
-    if constexpr (kFast) {
-      // The worst kept against the best left out (there may be none).
-      const Key above = __reduce_min_sync(kFull, kept ? mine : 0xffffffffu);
-      const Key below = __reduce_max_sync(kFull, kept ? 0u : mine);
-      if ((scored || sums) && below != 0) {
-        const float v = key_value(above, F());
-        near = v - key_value(below, F()) <= a.group_top * bound(v);
-      }
-    }
-    if (a.group_lanes > 0) {
-      if (((kept_mask >> (lane / a.group_lanes)) & 1u) == 0) {
-#pragma unroll kUnroll
-        for (int j = 0; j < EPL; ++j) key[j] = 0;
-      }
-    } else {
-#pragma unroll kUnroll
-      for (int j = 0; j < EPL; ++j)
-        if (key[j] != 0 && ((kept_mask >> ((uint32_t)(e0 + j) * a.group_magic >> 20)) & 1u) == 0) key[j] = 0;
-    }
+    const Key mine = __shfl_sync(kFull, total(k1, k2), lane * a.group_lanes & 31);
+    return lane < a.groups ? mine : 0;
   }
+  Key mine = 0;
+#pragma unroll 1
+  for (int g = 0; g < a.groups; ++g) {
+    Key k1 = 0, k2 = 0;  // this lane's best two
+#pragma unroll kUnroll
+    for (int j = 0; j < EPL; ++j) {
+      if ((int)((uint32_t)(e0 + j) * a.group_magic >> 20) != g) continue;
+      const Key k = value(j), lower = k < k1 ? k : k1;
+      k1 = k > k1 ? k : k1;
+      k2 = lower > k2 ? lower : k2;
+    }
+    const Key best = warp_max_key(k1);
+    const unsigned at = __ballot_sync(kFull, k1 == best);
+    const Key next = warp_max_key(lane == __ffs(at) - 1 ? k2 : k1);
+    if (lane == g) mine = total(best, next);
+  }
+  return mine;
+}
 
-  // topk times the best key of the warp.  A lane keeps the best of its own experts;
-  // the lane whose expert was taken looks again.  One more round, where
-  // neighbours are watched, for the best left out.
-  if (lane < a.topk) picks[lane] = -1;
-  __syncwarp();
-  const bool watch = kFast && scored;
-  const int rounds = watch ? a.topk + 1 : a.topk;
-  Key best = 0;
-  int best_j = 0;
-#pragma unroll kUnroll
-  for (int j = 0; j < EPL; ++j)
-    if (key[j] > best) {
-      best = key[j];
-      best_j = j;
-    }
-  float last = INFINITY;
+// The topk_groups best of the groups' keys, as a mask; a group's rank counts the
+// better ones.
+template <typename Key>
+NVM_DEV unsigned best_groups(const RouteArgs& a, Key mine, Key none) {
+  const int lane = threadIdx.x & 31;
+  int rank = 0;
 #pragma unroll 1
-  for (int s = 0; s < rounds; ++s) {
-    const Key top = warp_max_key(best);
-    if (top == 0) break;
-    if (watch) {
-      const float v = (float)key_value(top, F());
-      near |= last - v <= bound(v);  // infinity - infinity is no near pair
-      last = v;
-    }
-    const unsigned at = __ballot_sync(kFull, best == top);
-    if (lane == __ffs(at) - 1) {
-      if (s < a.topk) picks[s] = e0 + best_j;
-      best = 0;
-      const int taken = best_j;
-#pragma unroll kUnroll
-      for (int j = 0; j < EPL; ++j) {
-        if (j == taken) key[j] = 0;
-        if (key[j] > best) {
-          best = key[j];
-          best_j = j;
-        }
-      }
-    }
+  for (int g = 0; g < a.groups; ++g) {
+    const Key v = __shfl_sync(kFull, mine, g);
+    rank += v > mine || (v == mine && g < lane);
   }
-  __syncwarp();
-  return near;
+  return __ballot_sync(kFull, mine > none && rank < a.topk_groups);
 }
 
 template <typename T>
@@ -272,7 +193,7 @@ NVM_DEV float logit_f32(uint16_t v) {
 
 // A NaN logit counts as -infinity (not choosable), +infinity as the largest
 // finite value.
-NVM_DEV float clean_logit(float v) { return v != v ? -INFINITY : fminf(v, FLT_MAX); }
+NVM_DEV float clean_logit(float v) { return fminf(or_minus_infinity(v), FLT_MAX); }
 
 template <typename T, int EPL>
 NVM_DEV void load_logits(const RouteArgs& a, const T* row, float (&l)[EPL]) {
@@ -296,33 +217,299 @@ NVM_DEV void load_logits(const RouteArgs& a, const T* row, float (&l)[EPL]) {
   }
 }
 
-// The FP64 selection of a row whose FP32 order is not certain, out of line; it
-// reads the row again, so nothing has to be kept for it.
-template <typename T, int EPL>
-__device__ __noinline__ void select_exactly(const RouteArgs& a, const T* row, float lmax, int* picks) {
-  float l[EPL];
-  load_logits<T, EPL>(a, row, l);
-  double zinv = 0.0;
+// The FP64 forms, for rows that FP32 cannot order: out of line, small, and reading
+// the row again, so that the common way keeps nothing for them.
+struct Scores64 {
+  double lmax, zinv;
+};
+
+template <typename T>
+__device__ __noinline__ Scores64 scores_exactly(const RouteArgs& a, const T* row, float lmax) {
+  Scores64 s{(double)lmax, 0.0};
   if (a.softmax) {
     double z = 0.0;
-    for (int j = 0; j < EPL; ++j) z += exp((double)l[j] - (double)lmax);
-    zinv = 1.0 / warp_sum(z);
+#pragma unroll 1
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) z += exp((double)clean_logit(logit_f32<T>(row[e])) - s.lmax);
+    s.zinv = 1.0 / warp_sum(z);
   }
-  select_experts<double, EPL>(a, l, (double)lmax, zinv, picks);
+  return s;
+}
+
+// Key of the choice value of expert e.
+template <typename T>
+__device__ __noinline__ uint64_t choice_exactly(const RouteArgs& a, const T* row, Scores64 s, int e) {
+  const float x = clean_logit(logit_f32<T>(row[e]));
+  if (x == -INFINITY) return 0;
+  const double p = a.softmax ? exp((double)x - s.lmax) * s.zinv : 1.0 / (1.0 + exp(-(double)x));
+  return order_key(or_minus_infinity(a.bias != nullptr ? p + (double)a.bias[e] : p));
+}
+
+template <typename T, int EPL>
+__device__ __noinline__ unsigned groups_exactly(const RouteArgs& a, const T* row, Scores64 s) {
+  const int e0 = (threadIdx.x & 31) * a.per_lane;
+  const uint64_t mine = group_scores<double, EPL>(a, [&](int j) -> uint64_t {
+    return j < a.per_lane && e0 + j < a.E ? choice_exactly<T>(a, row, s, e0 + j) : 0;
+  });
+  return best_groups(a, mine, KeyOf<double>::none);
+}
+
+// The whole choice among the experts of the groups of `mask`: topk times the best.
+template <typename T, int EPL>
+__device__ __noinline__ void pick_exactly(const RouteArgs& a, const T* row, Scores64 s, unsigned mask, Picks& picks) {
+  const int lane = threadIdx.x & 31, e0 = lane * a.per_lane;
+  uint64_t key[EPL];
+#pragma unroll 1
+  for (int j = 0; j < EPL; ++j) {
+    key[j] = 0;
+    if (j < a.per_lane && e0 + j < a.E && in_mask(a, mask, e0 + j)) key[j] = choice_exactly<T>(a, row, s, e0 + j);
+  }
+#pragma unroll 1
+  for (int r = 0; r < a.topk; ++r) {
+    uint64_t best = 0;
+    int at = 0;
+#pragma unroll 1
+    for (int j = 0; j < EPL; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        at = j;
+      }
+    const uint64_t top = warp_max_key(best);
+    if (top <= KeyOf<double>::none) break;
+    if (lane == __ffs(__ballot_sync(kFull, best == top)) - 1) {
+      picks.id[r] = e0 + at;
+      picks.logit[r] = clean_logit(logit_f32<T>(row[e0 + at]));
+      key[at] = 0;
+    }
+  }
+  __syncwarp();
+}
+
+// The order of the n candidates by their FP64 values.
+template <typename T>
+__device__ __noinline__ void rank_exactly(const RouteArgs& a, const T* row, Scores64 s, int n, Picks& picks) {
+  const int lane = threadIdx.x & 31;
+  const int e = lane < n ? picks.expert[lane] : 0;
+  const uint64_t key = lane < n ? choice_exactly<T>(a, row, s, e) : 0;
+  int rank = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const uint64_t k = __shfl_sync(kFull, key, i);
+    rank += k > key || (k == key && i < lane);
+  }
+  if (lane < n && rank < a.topk) {
+    picks.id[rank] = e;
+    picks.logit[rank] = picks.found[lane];
+  }
+  __syncwarp();
+}
+
+// The selection, into picks.id[0 .. topk).  l[j] is the logit of expert per_lane *
+// lane + j (-infinity: not choosable), lmax and zinv the softmax's maximum and
+// 1 / sum.
+template <typename T, int EPL>
+NVM_DEV void select_experts(const RouteArgs& a, const T* row, const float (&l)[EPL], float lmax, float zinv,
+                            Picks& picks) {
+  constexpr uint32_t kNone = KeyOf<float>::none;
+  const int lane = threadIdx.x & 31, e0 = lane * a.per_lane;
+  const bool scored = a.bias != nullptr;  // the choice is s + bias; else the logit
+  // Error of an FP32 s.  Sigmoid: the exponential is off by (2 + 1.2 |x|) 2^-23 of
+  // its value, which s (1 - s) weighs to under 2^-23; 1 + exp and the quotient add
+  // 2^-24 and 2^-22: under 2^-21.  Softmax, in units of the largest score 1 / sum:
+  // the difference and the exponential as much, the sum EPL + 5 roundings.  s + bias
+  // adds 2^-24 of its value.  Twice that for two neighbours.
+  const float unit = a.softmax ? zinv * (8 + 2 * (EPL + 5)) * 0x1p-23f : 0x1p-20f;
+  auto bound = [&](float v) { return unit + fabsf(v) * 0x1p-23f; };
+  auto score = [&](float x) { return a.softmax ? __expf(x - lmax) * zinv : __fdividef(1.0f, 1.0f + __expf(-x)); };
+
+  uint32_t key[EPL];
+  if (scored) {
+    float b[EPL];
+    if (a.vec_bias) {
+      constexpr int kPer = EPL < 4 ? EPL : 4;
+      struct alignas(4 * kPer) Piece {
+        float v[kPer];
+      };
+#pragma unroll
+      for (int i = 0; i < EPL / kPer; ++i) {
+        const Piece p = reinterpret_cast<const Piece*>(a.bias + e0)[i];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) b[i * kPer + j] = p.v[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) b[j] = j < a.per_lane && e0 + j < a.E ? __ldg(a.bias + e0 + j) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = l[j] == -INFINITY ? 0 : order_key(or_minus_infinity(score(l[j]) + b[j]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = order_key(l[j]);
+  }
+
+  unsigned mask = 1u;
+  if (a.groups > 1) {
+    const bool sums = a.group_top > 1;
+    const uint32_t mine = group_scores<float, EPL>(a, [&](int j) -> uint32_t {
+      return scored || !sums || key[j] <= kNone ? key[j] : order_key(score(l[j]));
+    });
+    mask = best_groups(a, mine, kNone);
+    if (scored || sums) {
+      // The worst kept against the best left out (there may be none).
+      const bool kept = ((mask >> lane) & 1u) != 0;
+      const uint32_t above = __reduce_min_sync(kFull, kept ? mine : 0xffffffffu);
+      const uint32_t below = __reduce_max_sync(kFull, kept ? 0u : mine);
+      if (below > kNone) {
+        const float v = key_value(above, 0.0f);
+        if (v - key_value(below, 0.0f) <= a.group_top * bound(v))
+          mask = groups_exactly<T, EPL>(a, row, scores_exactly<T>(a, row, lmax));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const bool stays = a.group_lanes > 0 ? ((mask >> (lane / a.group_lanes)) & 1u) != 0 : in_mask(a, mask, e0 + j);
+      if (!stays) key[j] = 0;
+    }
+  }
+
+  // Every one of the topk best experts is at least the topk-th best of the lanes'
+  // bests.  Usually few others are (9 of 256 experts for 8): these candidates go
+  // to one lane each, and a candidate's rank counts the better ones.  Where FP32
+  // is not exact, what is within its error below them is a candidate too.
+  picks.id[lane] = -1;
+  picks.key[lane] = 0;
+  uint32_t best = key[0];
+#pragma unroll
+  for (int j = 1; j < EPL; ++j) best = key[j] > best ? key[j] : best;
+  uint32_t floor = 0, rest = best;
+#pragma unroll 1
+  for (int s = 0; s < a.topk; ++s) {
+    floor = __reduce_max_sync(kFull, rest);
+    if (rest == floor) rest = 0;
+  }
+  auto candidates = [&](uint32_t from) {  // of this lane
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) c += key[j] >= from;
+    return c;
+  };
+  if (floor <= kNone) floor = kNone + 1;
+  int n = __reduce_add_sync(kFull, candidates(floor));
+  if (n > 32) {
+    // Bisect for a higher bar that topk to 32 experts pass (there is none where
+    // too many are equal).
+    uint32_t over = __reduce_max_sync(kFull, best) + 1;
+#pragma unroll 1
+    while (over - floor > 1 && n > 32) {
+      const uint32_t middle = floor + (over - floor) / 2;
+      const int c = __reduce_add_sync(kFull, candidates(middle));
+      if (c < a.topk) {
+        over = middle;
+      } else {
+        floor = middle;
+        n = c;
+      }
+    }
+  }
+  if (scored) {
+    const float v = key_value(floor, 0.0f);
+    const float under = v - bound(v);
+    if (under < v) floor = order_key(under);  // not of an infinity
+    if (floor <= kNone) floor = kNone + 1;
+  }
+  const int count = candidates(floor);
+  int upto = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, upto, o);
+    if (lane >= o) upto += v;
+  }
+  n = __shfl_sync(kFull, upto, 31);
+  __syncwarp();
+  if (n <= 32) {
+    if (count > 0) {
+      int at = upto - count;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if (key[j] >= floor) {
+          picks.key[at] = key[j];
+          picks.expert[at] = e0 + j;
+          picks.found[at++] = l[j];
+        }
+    }
+    __syncwarp();
+    const uint2 c = make_uint2(picks.key[lane], (uint32_t)picks.expert[lane]);
+    const float logit = picks.found[lane];
+    int rank = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; i += 4) {
+      const uint4 k = *reinterpret_cast<const uint4*>(picks.key + i);
+      // Equal keys: found in the order of their index.
+      rank += k.x > c.x || (k.x == c.x && i < lane);
+      rank += k.y > c.x || (k.y == c.x && i + 1 < lane);
+      rank += k.z > c.x || (k.z == c.x && i + 2 < lane);
+      rank += k.w > c.x || (k.w == c.x && i + 3 < lane);
+    }
+    if (lane < n && rank < a.topk) {
+      picks.id[rank] = (int)c.y;
+      picks.logit[rank] = logit;
+    }
+    if (scored) {
+      if (lane < n) picks.ranked[rank] = c;
+      __syncwarp();
+      bool near = false;
+      if (lane + 1 < n && lane < a.topk) {
+        const uint2 p = picks.ranked[lane], q = picks.ranked[lane + 1];
+        const float v = key_value(p.x, 0.0f);
+        near = v - key_value(q.x, 0.0f) <= bound(v);
+        // Equal logits and biases are equal in any arithmetic.
+        if (near && p.x == q.x) near = row[p.y] != row[q.y] || a.bias[p.y] != a.bias[q.y];
+      }
+      if (__any_sync(kFull, near)) rank_exactly<T>(a, row, scores_exactly<T>(a, row, lmax), n, picks);
+    }
+    __syncwarp();
+    return;
+  }
+
+  // Otherwise (many equal values, or topk near 32) topk times the best key of the
+  // warp; the lane whose expert was taken looks again.
+  if (scored) {
+    pick_exactly<T, EPL>(a, row, scores_exactly<T>(a, row, lmax), a.groups > 1 ? mask : 0xffffffffu, picks);
+    return;
+  }
+#pragma unroll 1
+  for (int s = 0; s < a.topk; ++s) {
+    const uint32_t top = warp_max_key(best);
+    if (top <= kNone) break;
+    if (lane == __ffs(__ballot_sync(kFull, best == top)) - 1) {
+      best = 0;
+      int taken = -1;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        if (taken < 0 && key[j] == top) {
+          taken = j;
+          key[j] = 0;
+          picks.logit[s] = l[j];
+        }
+        best = key[j] > best ? key[j] : best;
+      }
+      picks.id[s] = e0 + taken;
+    }
+  }
+  __syncwarp();
 }
 
 }  // namespace
 
 template <typename T, int EPL>
-__global__ void __launch_bounds__(32 * kMaxWarps, EPL <= 8 ? 4 : EPL == 16 ? 2 : 1) route_topk_kernel(const RouteArgs a) {
-  __shared__ int s_picks[kMaxWarps][32];
+__global__ void __launch_bounds__(32 * kMaxWarps, EPL <= 8 ? 8 : EPL == 16 ? 6 : 4) route_topk_kernel(const RouteArgs a) {
+  __shared__ Picks s_picks[kMaxWarps];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const uint32_t t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= a.M) return;
   const T* row = static_cast<const T*>(a.logits) + (uint64_t)t * a.ld;
-  int* picks = s_picks[threadIdx.x >> 5];
+  Picks& picks = s_picks[threadIdx.x >> 5];
 
   float l[EPL];
   load_logits<T, EPL>(a, row, l);
@@ -341,13 +528,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps, EPL <= 8 ? 4 : EPL == 16 ? 2 :
       zinv = 1.0f / warp_sum(z);
     }
   }
-  if (select_experts<float, EPL>(a, l, lmax, zinv, picks)) select_exactly<T, EPL>(a, row, lmax, picks);
+  select_experts<T, EPL>(a, row, l, lmax, zinv, picks);
 
   // Weights.  Renormalised ones are formed relative to the largest chosen
   // logit, so they are never 0 / 0: softmax exp(l - top); sigmoid
   // exp(l - base) / (1 + exp(l)) with base = min(0, top).
-  const int id = lane < a.topk ? picks[lane] : -1;
-  const float x = id >= 0 ? clean_logit(logit_f32<T>(__ldg(row + id))) : -INFINITY;
+  const int id = picks.id[lane];
+  const float x = id >= 0 ? picks.logit[lane] : -INFINITY;
   float base = a.softmax ? lmax : 0.0f;
   if (a.renorm) {
     base = key_value(__reduce_max_sync(kFull, order_key(x)), 0.0f);
@@ -357,10 +544,15 @@ __global__ void __launch_bounds__(32 * kMaxWarps, EPL <= 8 ? 4 : EPL == 16 ? 2 :
   if (id >= 0) {
     const float low = expf(fminf(x, a.softmax ? x : 0.0f) - base);
     w = low;
-    if (!a.softmax) w = x > 0.0f ? 1.0f / (1.0f + expf(-x)) : low / (1.0f + expf(x));
+    if (!a.softmax) w = x > 0.0f ? __fdividef(1.0f, 1.0f + expf(-x)) : __fdividef(low, 1.0f + expf(x));
   }
   float norm = a.softmax ? zinv : 1.0f;
-  if (a.renorm) norm = 1.0f / warp_sum(w);
+  if (a.renorm) {
+    float sum = w;  // of lanes 0 .. topk - 1, the others' weights are 0
+#pragma unroll 1
+    for (int o = 1; o < a.topk; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    norm = __fdividef(1.0f, sum);
+  }
   if (lane < a.topk) {
     const uint64_t at = (uint64_t)t * a.topk + lane;
     a.ids[at] = id;
@@ -410,6 +602,8 @@ cudaError_t launch_route_topk(const void* logits, bool logits_f32, uint64_t ld, 
   const uint32_t lane_bytes = (uint32_t)a.per_lane * (logits_f32 ? 4 : 2), piece = lane_bytes < 16 ? lane_bytes : 16;
   a.vec = r.num_experts % 32 == 0 && (a.per_lane & (a.per_lane - 1)) == 0 &&
           reinterpret_cast<uintptr_t>(logits) % piece == 0 && ld * (logits_f32 ? 4 : 2) % piece == 0;
+  a.vec_bias = r.num_experts % 32 == 0 && (a.per_lane & (a.per_lane - 1)) == 0 &&
+               reinterpret_cast<uintptr_t>(r.bias) % (a.per_lane < 4 ? 4 * a.per_lane : 16) == 0;
   a.softmax = r.softmax;
   a.renorm = r.renormalize;
   a.scale = r.scale;
