@@ -525,8 +525,8 @@ NVFP4_MOE_API int nvfp4_moe_transpose_concat(const uint8_t* const* packed_parts,
  * the routing that feeds it, and the 8-bit products next to it.  The pages name
  * no launcher for them; conventions (device pointers, streams, status codes,
  * programmatic launch order) are those of the calls above.  None of them takes
- * a workspace or keeps anything between calls.  num_tokens (num_rows) == 0
- * launches nothing.
+ * a workspace or keeps anything between calls.  Row distances (ld...) are at most
+ * 2^30 elements.  num_tokens (num_rows) == 0 launches nothing.
  *
  * Element types of their arguments.  F32 and BF16 are the types of tensors;
  * INT8 (two's complement, codes -127..127 written) and E4M3 (finite "FN"
@@ -545,43 +545,27 @@ typedef enum {
 } nvfp4_moe_score;
 
 /*
- * A router (host struct, read during the call).
- *   bias         DEVICE f32 [num_experts] added to the scores for the choice
- *                only (balance), or NULL
- *   num_groups   consecutive groups of num_experts / num_groups experts; 1: none
- *   topk_groups  groups a token may choose from, 1..num_groups
- *   group_top    a group's score: the sum of its 1 or 2 best choice values
- *   score        nvfp4_moe_score
- *   renormalize  non-zero: a token's weights are divided by their sum
- *   scale        factor on every weight
- */
-typedef struct {
-  const float* bias;
-  uint32_t num_experts;
-  uint32_t topk;
-  uint32_t num_groups;
-  uint32_t topk_groups;
-  uint32_t group_top;
-  int32_t score;
-  int32_t renormalize;
-  float scale;
-} nvfp4_moe_router;
-
-/*
  * Routing: the topk experts of each token and their weights, as
  * nvfp4_moe_route_sort, nvfp4_moe_blend and the forward calls take them.
  *
+ * Arguments (a HOST struct, read during the call):
  *   logits        bf16 or f32 [num_tokens, num_experts], rows ld elements apart
+ *   bias          f32 [num_experts] added to the scores for the choice only
+ *                 (balance), or NULL
  *   topk_ids      i32 [num_tokens, topk]  out, contiguous: the chosen experts,
  *                 best first
  *   topk_weights  f32 [num_tokens, topk]  out: their scores (without bias),
- *                 renormalised if asked, times scale
+ *                 divided by their sum if renormalize is not 0, times scale
+ *   num_groups    consecutive groups of num_experts / num_groups experts; 1: none
+ *   topk_groups   groups a token may choose from
+ *   group_top     a group's score: the sum of its 1 or 2 best choice values
+ *   logits_type, score   nvfp4_moe_type, nvfp4_moe_score
  *
  * A token's choice value of expert e is s[e] + bias[e], without a bias l[e]
  * (the scores are monotone in it); with num_groups > 1 the topk_groups groups
  * with the best group scores stay (without a bias and with group_top 1 the best
  * logit is a group's score, with group_top 2 the sum of its two best scores);
- * then the topk best choice values, compared exactly (rows that FP32 cannot
+ * then the topk best choice values, compared exactly (values that FP32 cannot
  * order are ordered in FP64), ties to the lower index.  An expert whose logit is
  * -infinity or NaN, or whose bias is, cannot be chosen (a masked expert; an
  * all-masked row is a padding token); a logit of +infinity counts as the
@@ -594,9 +578,25 @@ typedef struct {
  * ld < num_experts, num_tokens * topk > 1<<24.  EINVAL: NULL or overlapping
  * pointers, unknown type or score, a scale that is not finite.
  */
-NVFP4_MOE_API int nvfp4_moe_route_topk(const void* logits, int logits_type, uint64_t ld,
-                                       uint32_t num_tokens, const nvfp4_moe_router* router,
-                                       int32_t* topk_ids, float* topk_weights, cudaStream_t stream);
+typedef struct {
+  const void* logits;
+  const float* bias;
+  int32_t* topk_ids;
+  float* topk_weights;
+  uint64_t ld;
+  uint32_t num_tokens;
+  uint32_t num_experts;
+  uint32_t topk;
+  uint32_t num_groups;
+  uint32_t topk_groups;
+  uint32_t group_top;
+  int32_t logits_type;
+  int32_t score;
+  int32_t renormalize;
+  float scale;
+} nvfp4_moe_route_args;
+
+NVFP4_MOE_API int nvfp4_moe_route_topk(const nvfp4_moe_route_args* args, cudaStream_t stream);
 
 /*
  * Root-mean-square norm with the residual's addition, output in BF16, in 8 bits
@@ -611,6 +611,7 @@ NVFP4_MOE_API int nvfp4_moe_route_topk(const void* logits, int logits_type, uint
  *
  * r, the mean and y are FP32; out and q are rounded once, from the unrounded r.
  *
+ * Arguments (a HOST struct, read during the call):
  *   x             bf16 or f32 [num_rows, hidden], rows ldx elements apart
  *   residual      bf16 or f32, rows ldr elements apart, or NULL
  *   residual_out  the residual's type [num_rows, hidden], contiguous, or NULL
@@ -627,23 +628,38 @@ NVFP4_MOE_API int nvfp4_moe_route_topk(const void* logits, int logits_type, uint
  * pointers, q without q_scale or the other way round, residual_out without
  * residual.
  */
-NVFP4_MOE_API int nvfp4_moe_add_rms_norm(const void* x, int x_type, uint64_t ldx,
-                                         const void* residual, int residual_type, uint64_t ldr,
-                                         void* residual_out, const void* weight, int weight_type,
-                                         float eps, uint32_t num_rows, uint32_t hidden,
-                                         uint16_t* out, void* q, int q_type, float* q_scale,
-                                         cudaStream_t stream);
+typedef struct {
+  const void* x;
+  const void* residual;
+  void* residual_out;
+  const void* weight;
+  uint16_t* out;
+  void* q;
+  float* q_scale;
+  uint64_t ldx;
+  uint64_t ldr;
+  uint32_t num_rows;
+  uint32_t hidden;
+  int32_t x_type;
+  int32_t residual_type;
+  int32_t weight_type;
+  int32_t q_type;
+  float eps;
+} nvfp4_moe_norm_args;
+
+NVFP4_MOE_API int nvfp4_moe_add_rms_norm(const nvfp4_moe_norm_args* args, cudaStream_t stream);
 
 /*
  * Product of 8-bit integer matrices with a scale per token and per channel:
  *
- *   out[m, j] = x_scale[m] * w_scale[j] * sum_k x[m, k] * w[j, k] + bias[j]
+ *   out[m, j] = x_scale[m] * w_scale[j] * sum_i x[m, i] * w[j, i] + bias[j]
  *
+ * Arguments (a HOST struct, read during the call):
  *   x        i8 [num_tokens, k], rows ldx bytes apart, 16-byte aligned
  *   x_scale  f32 [num_tokens]
  *   w        i8 [n, k], contiguous, 16-byte aligned
  *   w_scale  f32 [n]        bias  f32 [n] or NULL
- *   out      bf16 or f32 [num_tokens, n], rows ldo elements apart
+ *   out      bf16 or f32 (out_type) [num_tokens, n], rows ldo elements apart
  *
  * The integer sums are exact, so the result does not depend on how the work is
  * split; scales and bias are applied in FP32 and the result is rounded once.
@@ -651,10 +667,22 @@ NVFP4_MOE_API int nvfp4_moe_add_rms_norm(const void* x, int x_type, uint64_t ldx
  * 16, ldo < n, n == 0.  EINVAL: unknown type, NULL or misaligned pointers, out
  * overlapping an input.
  */
-NVFP4_MOE_API int nvfp4_moe_int8_matmul(const int8_t* x, uint64_t ldx, const float* x_scale,
-                                        const int8_t* w, const float* w_scale, const float* bias,
-                                        void* out, int out_type, uint64_t ldo, uint32_t num_tokens,
-                                        uint32_t n, uint32_t k, cudaStream_t stream);
+typedef struct {
+  const int8_t* x;
+  const float* x_scale;
+  const int8_t* w;
+  const float* w_scale;
+  const float* bias;
+  void* out;
+  uint64_t ldx;
+  uint64_t ldo;
+  uint32_t num_tokens;
+  uint32_t n;
+  uint32_t k;
+  int32_t out_type;
+} nvfp4_moe_int8_args;
+
+NVFP4_MOE_API int nvfp4_moe_int8_matmul(const nvfp4_moe_int8_args* args, cudaStream_t stream);
 
 /* Host helper: launch bound on active experts, min(num_experts, num_pairs). */
 NVFP4_MOE_API uint32_t nvfp4_moe_active_cap(uint32_t num_experts, uint32_t num_pairs);

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -28,7 +29,6 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 c_void_p = ctypes.c_void_p
 c_u32 = ctypes.c_uint32
-c_u64 = ctypes.c_uint64
 c_int = ctypes.c_int
 
 
@@ -48,13 +48,6 @@ class Buffers(ctypes.Structure):
     _fields_ = [("expert_offsets", c_void_p), ("sorted_pair_ids", c_void_p), ("pair_pos", c_void_p),
                 ("active_experts", c_void_p), ("active_count", c_void_p), ("status", c_void_p),
                 ("act", c_void_p), ("y", c_void_p), ("out_f32", c_void_p), ("out_bf16", c_void_p)]
-
-
-class Router(ctypes.Structure):
-    """nvfp4_moe_router."""
-    _fields_ = [("bias", c_void_p), ("num_experts", c_u32), ("topk", c_u32), ("num_groups", c_u32),
-                ("topk_groups", c_u32), ("group_top", c_u32), ("score", ctypes.c_int32),
-                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 PATH_AUTO, PATH_DECODE, PATH_PREFILL = 0, 1, 2
@@ -117,13 +110,9 @@ _sig = {
                                            c_void_p, c_void_p, c_void_p]),
     "nvfp4_moe_shard_nvfp4": (c_int, [c_void_p, c_void_p, c_u32, c_u32, c_u32, c_int, c_u32, c_u32,
                                       c_void_p, c_void_p, c_void_p]),
-    "nvfp4_moe_route_topk": (c_int, [c_void_p, c_int, c_u64, c_u32, ctypes.POINTER(Router), c_void_p,
-                                     c_void_p, c_void_p]),
-    "nvfp4_moe_add_rms_norm": (c_int, [c_void_p, c_int, c_u64, c_void_p, c_int, c_u64, c_void_p,
-                                       c_void_p, c_int, ctypes.c_float, c_u32, c_u32, c_void_p,
-                                       c_void_p, c_int, c_void_p, c_void_p]),
-    "nvfp4_moe_int8_matmul": (c_int, [c_void_p, c_u64, c_void_p, c_void_p, c_void_p, c_void_p,
-                                      c_void_p, c_int, c_u64, c_u32, c_u32, c_u32, c_void_p]),
+    "nvfp4_moe_route_topk": (c_int, [ctypes.c_char_p, c_void_p]),
+    "nvfp4_moe_add_rms_norm": (c_int, [ctypes.c_char_p, c_void_p]),
+    "nvfp4_moe_int8_matmul": (c_int, [ctypes.c_char_p, c_void_p]),
     "nvfp4_moe_workspace_bytes": (ctypes.c_size_t, [c_u32, c_u32, c_u32, c_u32]),
     "nvfp4_moe_device_error": (c_int, [c_int]),
     "nvfp4_moe_wait_selftest": (c_int, [c_u32, c_int, c_void_p]),
@@ -468,7 +457,18 @@ def forward_nongated(x, topk_ids, topk_weights, up: ExpertTables, down: ExpertTa
 
 # --- the operators around the forward ------------------------------------------
 # Their rows may be strided views, and they run on the device of their tensors,
-# on that device's current stream unless one is given.
+# on that device's current stream unless one is given.  Their arguments go over
+# as one packed struct (the library reads it during the call): a decode step
+# makes these calls in microseconds, and ctypes takes 0.1 us per argument.  Each
+# call tests its tensors in one expression of cheap attributes; only if that fails
+# does it look for what is wrong (or for what the expression does not know).
+
+_ROUTE_ARGS = struct.Struct("PPPPQIIIIIIiiif")   # nvfp4_moe_route_args
+_NORM_ARGS = struct.Struct("PPPPPPPQQIIiiiif")   # nvfp4_moe_norm_args
+_INT8_ARGS = struct.Struct("PPPPPPQQIIIi")       # nvfp4_moe_int8_args
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
 
 def _rows(t: torch.Tensor, name: str):
     """(rows, columns, elements between rows) of a 2-D tensor with unit inner stride."""
@@ -501,33 +501,33 @@ def _matrix(t: torch.Tensor, m: int, n: int, dev: int, name: str, dtype=None) ->
     return _on(t, dev, name, dtype)
 
 
-def _float_type(t: torch.Tensor, name: str) -> int:
-    code = _FLOAT_TYPES.get(t.dtype)
+def _type_code(t: torch.Tensor, name: str, codes=_FLOAT_TYPES) -> int:
+    code = codes.get(t.dtype)
     if code is None:
-        raise TypeError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+        raise TypeError(f"{name}: expected one of {[str(d) for d in codes]}, got {t.dtype}")
     return code
-
-
-def _launch(name: str, dev: int, stream, *args) -> None:
-    """Call the entry point with the tensors' device current."""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        stream = _stream(stream)
-    fn = getattr(_lib, name)
-    if torch.cuda.current_device() == dev:
-        status = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, stream)
-    if status != 0:
-        raise NVFP4MoEError(name, status)
 
 
 def _cuda_device(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
     return t.get_device()
+
+
+def _launch(name: str, fn, layout: struct.Struct, fields, dev: int, stream) -> None:
+    """Call the entry point with the tensors' device current."""
+    try:
+        args = layout.pack(*fields)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"{name}: argument out of range ({e})") from None
+    stream = _current_stream(dev) if stream is None else _stream(stream)
+    if _current_device() == dev:
+        status = fn(args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(args, stream)
+    if status != 0:
+        raise NVFP4MoEError(name, status)
 
 
 def route_topk(logits, topk_ids, topk_weights, *, score="softmax", bias=None, num_groups=1,
@@ -540,21 +540,29 @@ def route_topk(logits, topk_ids, topk_weights, *, score="softmax", bias=None, nu
     ``num_groups`` > 1 a token chooses among the experts of its ``topk_groups`` best
     groups (by the sum of a group's ``group_top`` best values).  Experts with a
     logit of -inf or NaN are never chosen; slots left over hold id -1, weight 0."""
-    if score not in SCORES:
+    code = SCORES.get(score)
+    if code is None:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
-    dev = _cuda_device(logits, "logits")
-    kind = _float_type(logits, "logits")
-    m, e, ld = _rows(logits, "logits")
-    if topk_ids.dim() != 2:
-        raise ValueError("topk_ids: must be [M, topk]")
-    k = topk_ids.shape[1]
-    ids = _matrix(topk_ids, m, k, dev, "topk_ids", torch.int32)
-    weights = _matrix(topk_weights, m, k, dev, "topk_weights", torch.float32)
-    b = None if bias is None else _vector(bias, e, dev, "bias")
-    router = Router(b, e, k, num_groups, topk_groups, group_top, SCORES[score],
-                    1 if renormalize else 0, scale)
-    _launch("nvfp4_moe_route_topk", dev, stream, logits.data_ptr(), kind, ld, m,
-            ctypes.byref(router), ids, weights)
+    dev, kind, shape, out = logits.get_device(), _FLOAT_TYPES.get(logits.dtype), logits.shape, topk_ids.shape
+    if (dev >= 0 and kind is not None and len(shape) == len(out) == 2 and out[0] == shape[0]
+            and logits.is_contiguous() and topk_weights.shape == out
+            and topk_ids.dtype is torch.int32 and topk_weights.dtype is torch.float32
+            and topk_ids.is_contiguous() and topk_weights.is_contiguous()
+            and topk_ids.get_device() == dev and topk_weights.get_device() == dev):
+        m, e = shape
+        k, ld, ids, weights = out[1], e, topk_ids.data_ptr(), topk_weights.data_ptr()
+    else:
+        dev, kind = _cuda_device(logits, "logits"), _type_code(logits, "logits")
+        m, e, ld = _rows(logits, "logits")
+        if len(out) != 2:
+            raise ValueError("topk_ids: must be [M, topk]")
+        k = out[1]
+        ids = _matrix(topk_ids, m, k, dev, "topk_ids", torch.int32)
+        weights = _matrix(topk_weights, m, k, dev, "topk_weights", torch.float32)
+    b = 0 if bias is None else _vector(bias, e, dev, "bias")
+    _launch("nvfp4_moe_route_topk", _lib.nvfp4_moe_route_topk, _ROUTE_ARGS,
+            (logits.data_ptr(), b, ids, weights, ld, m, e, k, num_groups, topk_groups, group_top,
+             kind, code, 1 if renormalize else 0, scale), dev, stream)
 
 
 def add_rms_norm(x, weight, eps, *, out=None, residual=None, residual_out=None, q=None,
@@ -566,36 +574,40 @@ def add_rms_norm(x, weight, eps, *, out=None, residual=None, residual_out=None, 
     residual's type), ``out`` (y in bf16), ``q`` with ``q_scale`` (y in int8 or
     float8_e4m3fn codes, one f32 scale per row).  ``residual_out`` may be
     ``residual`` itself."""
-    dev = _cuda_device(x, "x")
-    kind = _float_type(x, "x")
-    m, h, ldx = _rows(x, "x")
+    dev, kind, shape = x.get_device(), _FLOAT_TYPES.get(x.dtype), x.shape
+    if dev >= 0 and kind is not None and len(shape) == 2 and x.is_contiguous():
+        m, h = shape
+        ldx = h
+    else:
+        dev, kind = _cuda_device(x, "x"), _type_code(x, "x")
+        m, h, ldx = _rows(x, "x")
+    w_kind = _type_code(weight, "weight")
     w = _vector(weight, h, dev, "weight", None)
-    w_kind = _float_type(weight, "weight")
-    r = r_out = None
-    r_kind = ldr = 0
+    r = r_out = r_kind = ldr = y = codes = scales = q_kind = 0
     if residual is not None:
-        r_kind = _float_type(residual, "residual")
-        rm, rh, ldr = _rows(residual, "residual")
-        if (rm, rh) != (m, h):
-            raise ValueError("residual: must have the shape of x")
-        r = _on(residual, dev, "residual")
+        r_kind = _type_code(residual, "residual")
+        if residual.shape == shape and residual.get_device() == dev and residual.is_contiguous():
+            r, ldr = residual.data_ptr(), h
+        else:
+            rm, rh, ldr = _rows(residual, "residual")
+            if (rm, rh) != (m, h):
+                raise ValueError("residual: must have the shape of x")
+            r = _on(residual, dev, "residual")
     if residual_out is not None:
         if residual is None:
             raise ValueError("residual_out given without residual")
         r_out = _matrix(residual_out, m, h, dev, "residual_out", residual.dtype)
-    y = None if out is None else _matrix(out, m, h, dev, "out", torch.bfloat16)
-    codes = scales = None
-    q_kind = 0
+    if out is not None:
+        y = _matrix(out, m, h, dev, "out", torch.bfloat16)
     if (q is None) != (q_scale is None):
         raise ValueError("q and q_scale belong together")
     if q is not None:
-        q_kind = _CODE_TYPES.get(q.dtype)
-        if q_kind is None:
-            raise TypeError(f"q: expected int8 or float8_e4m3fn, got {q.dtype}")
+        q_kind = _type_code(q, "q", _CODE_TYPES)
         codes = _matrix(q, m, h, dev, "q")
         scales = _vector(q_scale, m, dev, "q_scale")
-    _launch("nvfp4_moe_add_rms_norm", dev, stream, x.data_ptr(), kind, ldx, r, r_kind, ldr, r_out,
-            w, w_kind, eps, m, h, y, codes, q_kind, scales)
+    _launch("nvfp4_moe_add_rms_norm", _lib.nvfp4_moe_add_rms_norm, _NORM_ARGS,
+            (x.data_ptr(), r, r_out, w, y, codes, scales, ldx, ldr, m, h, kind, r_kind, w_kind, q_kind,
+             eps), dev, stream)
 
 
 def int8_matmul(x_q, x_scale, w_q, w_scale, out, *, bias=None, stream=None) -> None:
@@ -603,19 +615,34 @@ def int8_matmul(x_q, x_scale, w_q, w_scale, out, *, bias=None, stream=None) -> N
     ``x_q`` int8 [M, K] (rows may be strided), ``w_q`` int8 [N, K], f32 scales [M] and
     [N], f32 ``bias`` [N] or None, ``out`` bf16 or f32 [M, N] (rows may be strided).
     K is a multiple of 16; the integer sums are exact."""
-    dev = _cuda_device(x_q, "x_q")
-    m, k, ldx = _rows(x_q, "x_q")
-    x = _on(x_q, dev, "x_q", torch.int8)
-    if w_q.dim() != 2:
-        raise ValueError("w_q: must be [N, K]")
-    n = w_q.shape[0]
-    w = _matrix(w_q, n, k, dev, "w_q", torch.int8)
-    xs = _vector(x_scale, m, dev, "x_scale")
-    ws = _vector(w_scale, n, dev, "w_scale")
-    b = None if bias is None else _vector(bias, n, dev, "bias")
-    kind = _float_type(out, "out")
-    om, on, ldo = _rows(out, "out")
-    if (om, on) != (m, n):
-        raise ValueError(f"out: must be [{m}, {n}]")
-    _launch("nvfp4_moe_int8_matmul", dev, stream, x, ldx, xs, w, ws, b, _on(out, dev, "out"), kind,
-            ldo, m, n, k)
+    dev, kind, shape, w_shape, i8, f32 = (x_q.get_device(), _FLOAT_TYPES.get(out.dtype), x_q.shape,
+                                          w_q.shape, torch.int8, torch.float32)
+    if (dev >= 0 and kind is not None and len(shape) == len(w_shape) == 2 and w_shape[1] == shape[1]
+            and out.shape == (shape[0], w_shape[0]) and x_scale.shape == shape[:1]
+            and w_scale.shape == w_shape[:1] and x_q.dtype is i8 and w_q.dtype is i8
+            and x_scale.dtype is f32 and w_scale.dtype is f32
+            and w_q.get_device() == dev and out.get_device() == dev
+            and x_scale.get_device() == dev and w_scale.get_device() == dev
+            and x_q.is_contiguous() and w_q.is_contiguous() and out.is_contiguous()
+            and x_scale.is_contiguous() and w_scale.is_contiguous()):
+        m, k = shape
+        n = w_shape[0]
+        ldx, ldo = k, n
+    else:
+        dev, kind = _cuda_device(x_q, "x_q"), _type_code(out, "out")
+        m, k, ldx = _rows(x_q, "x_q")
+        if len(w_shape) != 2:
+            raise ValueError("w_q: must be [N, K]")
+        n = w_shape[0]
+        _on(x_q, dev, "x_q", i8)
+        _matrix(w_q, n, k, dev, "w_q", i8)
+        _vector(x_scale, m, dev, "x_scale")
+        _vector(w_scale, n, dev, "w_scale")
+        om, on, ldo = _rows(out, "out")
+        if (om, on) != (m, n):
+            raise ValueError(f"out: must be [{m}, {n}]")
+        _on(out, dev, "out")
+    b = 0 if bias is None else _vector(bias, n, dev, "bias")
+    _launch("nvfp4_moe_int8_matmul", _lib.nvfp4_moe_int8_matmul, _INT8_ARGS,
+            (x_q.data_ptr(), x_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), b,
+             out.data_ptr(), ldx, ldo, m, n, k, kind), dev, stream)

@@ -648,6 +648,9 @@ bool span_same(const Span& a, const Span& b) {
   return a.p == b.p && a.row == b.row && (a.pitch == b.pitch || a.rows == 1);
 }
 
+// Elements between rows at most: 2^31 rows of them stay within 64-bit offsets.
+constexpr uint64_t kMaxPitch = 1ull << 30;
+
 bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 
 bool float_type(int t) { return t == NVFP4_MOE_BF16 || t == NVFP4_MOE_F32; }
@@ -656,14 +659,12 @@ uint64_t float_bytes(int t) { return t == NVFP4_MOE_F32 ? 4 : 2; }
 
 }  // namespace
 
-int nvfp4_moe_route_topk(const void* logits, int logits_type, uint64_t ld, uint32_t num_tokens,
-                         const nvfp4_moe_router* r, int32_t* topk_ids, float* topk_weights,
-                         cudaStream_t stream) {
-  if (r == nullptr || !float_type(logits_type)) return NVFP4_MOE_EINVAL;
+int nvfp4_moe_route_topk(const nvfp4_moe_route_args* r, cudaStream_t stream) {
+  if (r == nullptr || !float_type(r->logits_type)) return NVFP4_MOE_EINVAL;
   if (r->score != NVFP4_MOE_SCORE_SOFTMAX && r->score != NVFP4_MOE_SCORE_SIGMOID) return NVFP4_MOE_EINVAL;
   if (!std::isfinite(r->scale)) return NVFP4_MOE_EINVAL;
   if (r->num_experts == 0 || r->num_experts > kMaxExperts || r->topk == 0 ||
-      r->topk > kMaxRouteTopk || ld < r->num_experts)
+      r->topk > kMaxRouteTopk || r->ld < r->num_experts || r->ld > kMaxPitch)
     return NVFP4_MOE_ESHAPE;
   if (r->num_groups == 0 || r->num_groups > kMaxRouteGroups || r->num_experts % r->num_groups != 0 ||
       r->topk_groups == 0 || r->topk_groups > r->num_groups)
@@ -672,17 +673,17 @@ int nvfp4_moe_route_topk(const void* logits, int logits_type, uint64_t ld, uint3
   if (r->group_top == 0 || r->group_top > 2 || r->group_top > per_group ||
       r->topk > r->topk_groups * per_group)
     return NVFP4_MOE_ESHAPE;
-  if ((uint64_t)num_tokens * r->topk > kMaxPairs) return NVFP4_MOE_ESHAPE;
-  if (num_tokens == 0) return NVFP4_MOE_OK;
-  if (logits == nullptr || topk_ids == nullptr || topk_weights == nullptr) return NVFP4_MOE_EINVAL;
-  if (misaligned(logits, float_bytes(logits_type)) || misaligned(r->bias, 4) ||
-      misaligned(topk_ids, 4) || misaligned(topk_weights, 4))
+  if ((uint64_t)r->num_tokens * r->topk > kMaxPairs) return NVFP4_MOE_ESHAPE;
+  if (r->num_tokens == 0) return NVFP4_MOE_OK;
+  if (r->logits == nullptr || r->topk_ids == nullptr || r->topk_weights == nullptr) return NVFP4_MOE_EINVAL;
+  if (misaligned(r->logits, float_bytes(r->logits_type)) || misaligned(r->bias, 4) ||
+      misaligned(r->topk_ids, 4) || misaligned(r->topk_weights, 4))
     return NVFP4_MOE_EINVAL;
-  if (ld > (1ull << 40)) return NVFP4_MOE_ESHAPE;
-  const uint64_t fb = float_bytes(logits_type), out_row = 4ull * r->topk;
-  const Span in{logits, num_tokens, r->num_experts * fb, ld * fb};
+  const uint64_t fb = float_bytes(r->logits_type), out_row = 4ull * r->topk;
+  const Span in{r->logits, r->num_tokens, r->num_experts * fb, r->ld * fb};
   const Span bias{r->bias, 1, 4ull * r->num_experts, 0};
-  const Span ids{topk_ids, num_tokens, out_row, out_row}, w{topk_weights, num_tokens, out_row, out_row};
+  const Span ids{r->topk_ids, r->num_tokens, out_row, out_row};
+  const Span w{r->topk_weights, r->num_tokens, out_row, out_row};
   if (span_overlap(in, ids) || span_overlap(in, w) || span_overlap(ids, w) || span_overlap(bias, ids) ||
       span_overlap(bias, w))
     return NVFP4_MOE_EINVAL;
@@ -696,40 +697,39 @@ int nvfp4_moe_route_topk(const void* logits, int logits_type, uint64_t ld, uint3
   c.softmax = r->score == NVFP4_MOE_SCORE_SOFTMAX;
   c.renormalize = r->renormalize != 0;
   c.scale = r->scale;
-  return status_of(launch_route_topk(logits, logits_type == NVFP4_MOE_F32, ld, num_tokens, c, topk_ids,
-                                     topk_weights, stream));
+  return status_of(launch_route_topk(r->logits, r->logits_type == NVFP4_MOE_F32, r->ld, r->num_tokens, c,
+                                     r->topk_ids, r->topk_weights, stream));
 }
 
-int nvfp4_moe_add_rms_norm(const void* x, int x_type, uint64_t ldx, const void* residual,
-                           int residual_type, uint64_t ldr, void* residual_out, const void* weight,
-                           int weight_type, float eps, uint32_t num_rows, uint32_t hidden,
-                           uint16_t* out, void* q, int q_type, float* q_scale, cudaStream_t stream) {
-  if (!float_type(x_type) || !float_type(weight_type) || (residual != nullptr && !float_type(residual_type)))
+int nvfp4_moe_add_rms_norm(const nvfp4_moe_norm_args* args, cudaStream_t stream) {
+  if (args == nullptr) return NVFP4_MOE_EINVAL;
+  const nvfp4_moe_norm_args& g = *args;
+  if (!float_type(g.x_type) || !float_type(g.weight_type) || (g.residual != nullptr && !float_type(g.residual_type)))
     return NVFP4_MOE_EINVAL;
-  if (!(eps > 0.0f) || !std::isfinite(eps)) return NVFP4_MOE_EINVAL;
-  if (hidden == 0 || hidden > kMaxNormHidden || num_rows > 0x7fffffffu || ldx < hidden ||
-      ldx > (1ull << 40) || (residual != nullptr && (ldr < hidden || ldr > (1ull << 40))))
+  if (!(g.eps > 0.0f) || !std::isfinite(g.eps)) return NVFP4_MOE_EINVAL;
+  if (g.hidden == 0 || g.hidden > kMaxNormHidden || g.num_rows > 0x7fffffffu || g.ldx < g.hidden ||
+      g.ldx > kMaxPitch || (g.residual != nullptr && (g.ldr < g.hidden || g.ldr > kMaxPitch)))
     return NVFP4_MOE_ESHAPE;
-  if (num_rows == 0) return NVFP4_MOE_OK;
-  if ((q == nullptr) != (q_scale == nullptr)) return NVFP4_MOE_EINVAL;
-  if (q != nullptr && q_type != NVFP4_MOE_INT8 && q_type != NVFP4_MOE_E4M3) return NVFP4_MOE_EINVAL;
-  if (residual == nullptr && residual_out != nullptr) return NVFP4_MOE_EINVAL;
-  if (out == nullptr && q == nullptr) return NVFP4_MOE_EINVAL;
-  if (x == nullptr || weight == nullptr) return NVFP4_MOE_EINVAL;
-  const uint64_t xb = float_bytes(x_type), wb = float_bytes(weight_type);
-  const uint64_t rb = residual != nullptr ? float_bytes(residual_type) : 2, h = hidden;
-  if (misaligned(x, xb) || misaligned(weight, wb) || misaligned(residual, rb) ||
-      misaligned(residual_out, rb) || misaligned(out, 2) || misaligned(q_scale, 4))
+  if (g.num_rows == 0) return NVFP4_MOE_OK;
+  if ((g.q == nullptr) != (g.q_scale == nullptr)) return NVFP4_MOE_EINVAL;
+  if (g.q != nullptr && g.q_type != NVFP4_MOE_INT8 && g.q_type != NVFP4_MOE_E4M3) return NVFP4_MOE_EINVAL;
+  if (g.residual == nullptr && g.residual_out != nullptr) return NVFP4_MOE_EINVAL;
+  if (g.out == nullptr && g.q == nullptr) return NVFP4_MOE_EINVAL;
+  if (g.x == nullptr || g.weight == nullptr) return NVFP4_MOE_EINVAL;
+  const uint64_t xb = float_bytes(g.x_type), wb = float_bytes(g.weight_type);
+  const uint64_t rb = g.residual != nullptr ? float_bytes(g.residual_type) : 2, h = g.hidden;
+  if (misaligned(g.x, xb) || misaligned(g.weight, wb) || misaligned(g.residual, rb) ||
+      misaligned(g.residual_out, rb) || misaligned(g.out, 2) || misaligned(g.q_scale, 4))
     return NVFP4_MOE_EINVAL;
   // Each element is read before the same thread writes it, so an output may
   // stand exactly on x or residual; any other overlap is refused.
-  const Span ins[3] = {{x, num_rows, h * xb, ldx * xb},
-                       {residual, num_rows, h * rb, ldr * rb},
-                       {weight, 1, h * wb, 0}};
-  const Span outs[4] = {{residual_out, num_rows, h * rb, h * rb},
-                        {out, num_rows, h * 2, h * 2},
-                        {q, num_rows, h, h},
-                        {q_scale, 1, 4ull * num_rows, 0}};
+  const Span ins[3] = {{g.x, g.num_rows, h * xb, g.ldx * xb},
+                       {g.residual, g.num_rows, h * rb, g.ldr * rb},
+                       {g.weight, 1, h * wb, 0}};
+  const Span outs[4] = {{g.residual_out, g.num_rows, h * rb, h * rb},
+                        {g.out, g.num_rows, h * 2, h * 2},
+                        {g.q, g.num_rows, h, h},
+                        {g.q_scale, 1, 4ull * g.num_rows, 0}};
   for (int o = 0; o < 4; ++o) {
     for (int i = 0; i < 3; ++i)
       if (span_overlap(ins[i], outs[o]) && (i == 2 || o > 1 || !span_same(ins[i], outs[o])))
@@ -738,61 +738,60 @@ int nvfp4_moe_add_rms_norm(const void* x, int x_type, uint64_t ldx, const void* 
       if (span_overlap(outs[p], outs[o])) return NVFP4_MOE_EINVAL;
   }
   NormConfig c{};
-  c.x = x;
-  c.residual = residual;
-  c.residual_out = residual_out;
-  c.weight = weight;
-  c.out = out;
-  c.q = q;
-  c.q_scale = q_scale;
-  c.ldx = ldx;
-  c.ldr = residual != nullptr ? ldr : 0;
-  c.rows = num_rows;
-  c.hidden = hidden;
-  c.q_kind = q_type == NVFP4_MOE_INT8 ? kQuantInt8 : kQuantE4M3;
-  c.x_f32 = x_type == NVFP4_MOE_F32;
-  c.residual_f32 = residual != nullptr && residual_type == NVFP4_MOE_F32;
-  c.weight_f32 = weight_type == NVFP4_MOE_F32;
-  c.eps = eps;
+  c.x = g.x;
+  c.residual = g.residual;
+  c.residual_out = g.residual_out;
+  c.weight = g.weight;
+  c.out = g.out;
+  c.q = g.q;
+  c.q_scale = g.q_scale;
+  c.ldx = g.ldx;
+  c.ldr = g.residual != nullptr ? g.ldr : 0;
+  c.rows = g.num_rows;
+  c.hidden = g.hidden;
+  c.q_kind = g.q_type == NVFP4_MOE_INT8 ? kQuantInt8 : kQuantE4M3;
+  c.x_f32 = g.x_type == NVFP4_MOE_F32;
+  c.residual_f32 = g.residual != nullptr && g.residual_type == NVFP4_MOE_F32;
+  c.weight_f32 = g.weight_type == NVFP4_MOE_F32;
+  c.eps = g.eps;
   return status_of(launch_add_rms_norm(c, stream));
 }
 
-int nvfp4_moe_int8_matmul(const int8_t* x, uint64_t ldx, const float* x_scale, const int8_t* w,
-                          const float* w_scale, const float* bias, void* out, int out_type,
-                          uint64_t ldo, uint32_t num_tokens, uint32_t n, uint32_t k,
-                          cudaStream_t stream) {
-  if (!float_type(out_type)) return NVFP4_MOE_EINVAL;
-  if (n == 0 || n > 0x7fffff00u || num_tokens > 0x7fffff00u || k == 0 || k % 16 != 0 || k > kMaxInt8K ||
-      ldx < k || ldx % 16 != 0 || ldx >= (1ull << 40) || ldo < n || ldo > (1ull << 40))
+int nvfp4_moe_int8_matmul(const nvfp4_moe_int8_args* args, cudaStream_t stream) {
+  if (args == nullptr) return NVFP4_MOE_EINVAL;
+  const nvfp4_moe_int8_args& g = *args;
+  if (!float_type(g.out_type)) return NVFP4_MOE_EINVAL;
+  if (g.n == 0 || g.n > 0x7fffff00u || g.num_tokens > 0x7fffff00u || g.k == 0 || g.k % 16 != 0 || g.k > kMaxInt8K ||
+      g.ldx < g.k || g.ldx % 16 != 0 || g.ldx > kMaxPitch || g.ldo < g.n || g.ldo > kMaxPitch)
     return NVFP4_MOE_ESHAPE;
-  if (num_tokens == 0) return NVFP4_MOE_OK;
-  if (x == nullptr || x_scale == nullptr || w == nullptr || w_scale == nullptr || out == nullptr)
+  if (g.num_tokens == 0) return NVFP4_MOE_OK;
+  if (g.x == nullptr || g.x_scale == nullptr || g.w == nullptr || g.w_scale == nullptr || g.out == nullptr)
     return NVFP4_MOE_EINVAL;
-  const uint64_t ob = float_bytes(out_type);
-  if (misaligned(x, 16) || misaligned(w, 16) || misaligned(x_scale, 4) || misaligned(w_scale, 4) ||
-      misaligned(bias, 4) || misaligned(out, ob))
+  const uint64_t ob = float_bytes(g.out_type);
+  if (misaligned(g.x, 16) || misaligned(g.w, 16) || misaligned(g.x_scale, 4) || misaligned(g.w_scale, 4) ||
+      misaligned(g.bias, 4) || misaligned(g.out, ob))
     return NVFP4_MOE_EINVAL;
-  const Span dst{out, num_tokens, n * ob, ldo * ob};
-  const Span ins[5] = {{x, num_tokens, k, ldx},
-                       {w, n, k, k},
-                       {x_scale, 1, 4ull * num_tokens, 0},
-                       {w_scale, 1, 4ull * n, 0},
-                       {bias, 1, 4ull * n, 0}};
+  const Span dst{g.out, g.num_tokens, g.n * ob, g.ldo * ob};
+  const Span ins[5] = {{g.x, g.num_tokens, g.k, g.ldx},
+                       {g.w, g.n, g.k, g.k},
+                       {g.x_scale, 1, 4ull * g.num_tokens, 0},
+                       {g.w_scale, 1, 4ull * g.n, 0},
+                       {g.bias, 1, 4ull * g.n, 0}};
   for (const Span& i : ins)
     if (span_overlap(i, dst)) return NVFP4_MOE_EINVAL;
   Int8MatmulArgs a{};
-  a.x = x;
-  a.x_scale = x_scale;
-  a.w = w;
-  a.w_scale = w_scale;
-  a.bias = bias;
-  a.out = out;
-  a.ldx = ldx;
-  a.ldo = ldo;
-  a.M = num_tokens;
-  a.N = n;
-  a.K = k;
-  a.out_f32 = out_type == NVFP4_MOE_F32;
+  a.x = g.x;
+  a.x_scale = g.x_scale;
+  a.w = g.w;
+  a.w_scale = g.w_scale;
+  a.bias = g.bias;
+  a.out = g.out;
+  a.ldx = g.ldx;
+  a.ldo = g.ldo;
+  a.M = g.num_tokens;
+  a.N = g.n;
+  a.K = g.k;
+  a.out_f32 = g.out_type == NVFP4_MOE_F32;
   return status_of(launch_int8_matmul(a, stream));
 }
 
