@@ -482,20 +482,26 @@ def _rows(t: torch.Tensor, name: str):
 
 def _on(t: torch.Tensor, dev: int, name: str, dtype=None) -> int:
     """The tensor's address, after checking its device and type."""
-    if t.get_device() != dev or not t.is_cuda:
+    if t.get_device() != dev:  # -1 on the CPU
         raise ValueError(f"{name}: must be a CUDA tensor on the same device as the others")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     return t.data_ptr()
 
 
 def _vector(t: torch.Tensor, n: int, dev: int, name: str, dtype=torch.float32) -> int:
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if (t.ndim == 1 and t.numel() == n and t.is_contiguous() and t.get_device() == dev
+            and (dtype is None or t.dtype is dtype)):
+        return t.data_ptr()
+    if t.ndim != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: must be a contiguous vector of {n} values")
     return _on(t, dev, name, dtype)
 
 
 def _matrix(t: torch.Tensor, m: int, n: int, dev: int, name: str, dtype=None) -> int:
+    if (t.shape == (m, n) and t.is_contiguous() and t.get_device() == dev
+            and (dtype is None or t.dtype is dtype)):
+        return t.data_ptr()
     if t.shape != (m, n) or not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous [{m}, {n}]")
     return _on(t, dev, name, dtype)
@@ -618,8 +624,9 @@ def int8_matmul(x_q, x_scale, w_q, w_scale, out, *, bias=None, stream=None) -> N
     dev, kind, shape, w_shape, i8, f32 = (x_q.get_device(), _FLOAT_TYPES.get(out.dtype), x_q.shape,
                                           w_q.shape, torch.int8, torch.float32)
     if (dev >= 0 and kind is not None and len(shape) == len(w_shape) == 2 and w_shape[1] == shape[1]
-            and out.shape == (shape[0], w_shape[0]) and x_scale.shape == shape[:1]
-            and w_scale.shape == w_shape[:1] and x_q.dtype is i8 and w_q.dtype is i8
+            and out.shape == (shape[0], w_shape[0]) and x_scale.ndim == 1 and w_scale.ndim == 1
+            and x_scale.numel() == shape[0] and w_scale.numel() == w_shape[0]
+            and x_q.dtype is i8 and w_q.dtype is i8
             and x_scale.dtype is f32 and w_scale.dtype is f32
             and w_q.get_device() == dev and out.get_device() == dev
             and x_scale.get_device() == dev and w_scale.get_device() == dev

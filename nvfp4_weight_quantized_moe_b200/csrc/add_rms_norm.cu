@@ -10,12 +10,14 @@
 // y: the residual's rounding to BF16 does not enter the norm.  Since y is
 // r * weight times one factor per row, q = r * weight * (Q / max|r * weight|):
 // max and mean square are reduced together, in one pass over a row that stays in
-// registers.
+// registers.  The product and the quotient keep their rounding errors until q is
+// rounded, so a code goes to the other neighbour less often than with the
+// division as written.
 //
-// Bound by HBM: each input is read once, each output written once.  A row
-// belongs to one warp (hidden up to 1024) or one CTA; each thread moves 16 bytes
-// per load where the pointers, strides and hidden allow it, single elements
-// where they do not.
+// Bound by HBM: each input is read once, each output written once (8192 x 4096
+// BF16 with residual: 42.9 us, 96 % of the copy bandwidth).  A row belongs to one
+// warp or one CTA; each thread moves 16 bytes per load where the pointers and
+// strides allow it, single elements where they do not.
 
 #include <type_traits>
 
@@ -146,12 +148,142 @@ NVM_DEV void store_codes(uint8_t* p, const float (&f)[VEC], int kind) {
   }
 }
 
+// VEC weights from `at` on.  Not `whole`: between pieces, so the pieces on either
+// side are loaded and shifted by at % 8 elements in three steps (two of 4 for
+// FP32); where those pass the end of the row, single elements are.
+template <int VEC>
+NVM_DEV void load_weights(const NormArgs& a, int at, bool whole, float (&w)[VEC]) {
+  if (a.weight_f32) {
+    const float* p = static_cast<const float*>(a.weight) + at;
+    if (whole) {
+      Raw<float, VEC> r;
+      load_raw(r, p);
+      to_float(r, w);
+      return;
+    }
+    if constexpr (VEC == 8) {
+      const int s = at & 3;
+      if (at - s + 12 <= a.hidden) {
+        float f[12];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(p - s) + i);
+          f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 10; ++i) f[i] = s & 2 ? f[i + 2] : f[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = s & 1 ? f[i + 1] : f[i];
+        return;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) w[j] = __ldg(p + j);
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(a.weight) + at;
+    if (whole) {
+      Raw<uint16_t, VEC> r;
+      load_raw(r, p);
+      to_float(r, w);
+      return;
+    }
+    if constexpr (VEC == 8) {
+      const int s = at & 7;
+      if (at - s + 16 <= a.hidden) {
+        const uint4 lo = __ldg(reinterpret_cast<const uint4*>(p - s)), hi = __ldg(reinterpret_cast<const uint4*>(p - s) + 1);
+        uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int i = 0; i < 6; ++i) u[i] = s & 4 ? u[i + 2] : u[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) u[i] = s & 2 ? u[i + 1] : u[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = s & 1 ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
+        unpack_bf16x8(make_uint4(u[0], u[1], u[2], u[3]), w);
+        return;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) w[j] = bf16_bits_to_f32(__ldg(p + j));
+  }
+}
+
+// r of VEC elements.
+template <typename XT, typename RT, typename RTs, int VEC>
+NVM_DEV void add(const Raw<XT, VEC>& rx, const Raw<RTs, VEC>& rr, float (&r)[VEC]) {
+  to_float(rx, r);
+  if constexpr (!std::is_same<RT, NoResidual>::value) {
+    float f[VEC];
+    to_float(rr, f);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) r[j] += f[j];
+  }
+}
+
+// First pass over VEC elements: r to residual_out, its squares into `sum` and,
+// for codes, the largest r * weight into `most`.
+template <typename XT, typename RT, typename RTs, int VEC>
+NVM_DEV void take(const NormArgs& a, uint64_t row, int at, const Raw<XT, VEC>& rx, const Raw<RTs, VEC>& rr,
+                  const float (&w)[VEC], float& sum, float& most) {
+  float r[VEC];
+  add<XT, RT>(rx, rr, r);
+  if (!std::is_same<RT, NoResidual>::value && a.res_out != nullptr)
+    store<VEC>(static_cast<RTs*>(a.res_out) + row * (uint64_t)a.hidden + at, r);
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) sum = fmaf(r[j], r[j], sum);
+  if (a.q_kind != kQuantNone) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) most = fmaxf(most, fabsf(r[j] * w[j]));
+  }
+}
+
+// Q / max|r * weight| as hi + lo; values below 2^-60, whose quotient would leave
+// FP32, are brought up by `lift` first (exact).  A row of zeros gives zeros.
+struct Step {
+  float lift, hi, lo;
+};
+NVM_DEV Step code_step(float most, float range) {
+  Step s{most < 0x1p-60f ? 0x1p64f : 1.0f, 0.0f, 0.0f};
+  if (most > 0.0f) {
+    const float m = most * s.lift;
+    s.hi = range / m;
+    const float lo = fmaf(-s.hi, m, range) / m;
+    s.lo = fabsf(lo) < INFINITY ? lo : 0.0f;  // not of an infinite row
+  }
+  return s;
+}
+
+// Second pass: the codes and the norm.
+template <typename XT, typename RT, typename RTs, int VEC>
+NVM_DEV void give(const NormArgs& a, uint64_t row, int at, const Raw<XT, VEC>& rx, const Raw<RTs, VEC>& rr,
+                  const float (&w)[VEC], const Step& step, float inv) {
+  const uint64_t o = row * (uint64_t)a.hidden + at;
+  float r[VEC], f[VEC];
+  add<XT, RT>(rx, rr, r);
+  if (a.q_kind != kQuantNone) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const float t = r[j] * w[j], off = fmaf(r[j], w[j], -t);  // t + off is the product
+      f[j] = fmaf(t * step.lift, step.hi, fmaf(t * step.lift, step.lo, off * step.lift * step.hi));
+    }
+    store_codes<VEC>(static_cast<uint8_t*>(a.q) + o, f, a.q_kind);
+  }
+  if (a.out != nullptr) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) r[j] = r[j] * w[j] * inv;
+    store<VEC>(a.out + o, r);
+  }
+}
+
 }  // namespace
 
 // blockDim = (threads per row, rows per CTA); threads per row is a multiple of
 // 32, and 32 whenever a CTA holds more than one row.  A thread holds NV pieces
-// of VEC elements, blockDim.x pieces apart.
-template <typename XT, typename RT, int VEC, int NV>
+// of VEC elements, blockDim.x pieces apart, as they were loaded: r is formed again
+// in the second pass, which keeps a piece in 4 to 16 registers and many rows on
+// their way.  Pieces of 8 lie on multiples of 8 elements of the tensors; with ENDS
+// a row that does not begin or end on one has up to 7 single elements at either
+// end, one each for the first threads.
+template <typename XT, typename RT, int VEC, int NV, bool ENDS>
 __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormArgs a) {
   constexpr bool kRes = !std::is_same<RT, NoResidual>::value;
   using RTs = typename std::conditional<kRes, RT, uint16_t>::type;
@@ -160,57 +292,53 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormArgs a) {
   griddep_launch_dependents();
   const uint64_t row = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= a.rows) return;  // whole warps: a row's threads leave together
-  const int H = a.hidden;
+  const int H = a.hidden, tid = (int)threadIdx.x;
   const XT* x = static_cast<const XT*>(a.x) + row * a.ldx;
   const RTs* res = static_cast<const RTs*>(a.res) + row * a.ldr;
+  int head = 0, body = H, single = H;  // elements before the pieces and in them; this thread's single one
+  if constexpr (ENDS) {
+    head = min(H, (int)((0 - row * (uint64_t)H) & (VEC - 1)));
+    body = (H - head) & ~(VEC - 1);
+    single = tid >= 2 * VEC ? H : tid < head ? tid : tid + body;
+  }
+  const bool whole = !ENDS || head == 0;
+  const bool lone = ENDS && single < H;
 
   Raw<XT, VEC> rx[NV];
   Raw<RTs, VEC> rr[NV];
+  Raw<XT, 1> lx;
+  Raw<RTs, 1> lr;
+  float w[VEC], lw[1];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int at = (i * (int)blockDim.x + (int)threadIdx.x) * VEC;
-    if (at < H) {
-      load_raw(rx[i], x + at);
-      if constexpr (kRes) load_raw(rr[i], res + at);
+    const int at = (i * (int)blockDim.x + tid) * VEC;
+    if (at < body) {
+      load_raw(rx[i], x + head + at);
+      if constexpr (kRes) load_raw(rr[i], res + head + at);
     }
   }
-  // r, then r * weight; the mean square of the one, the largest of the other.
-  float v[NV][VEC];
+  if (lone) {
+    load_raw(lx, x + single);
+    if constexpr (kRes) load_raw(lr, res + single);
+    load_weights<1>(a, single, true, lw);
+  }
+  // One piece per thread: its weights come with it.
+  if (NV == 1 && tid * VEC < body) load_weights<VEC>(a, head + tid * VEC, whole, w);
+
   float sum = 0.0f, most = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int at = (i * (int)blockDim.x + (int)threadIdx.x) * VEC;
-    if (at >= H) continue;
-    float w[VEC];
-    if (a.weight_f32) {
-      Raw<float, VEC> rw;
-      load_raw(rw, static_cast<const float*>(a.weight) + at);
-      to_float(rw, w);
-    } else {
-      Raw<uint16_t, VEC> rw;
-      load_raw(rw, static_cast<const uint16_t*>(a.weight) + at);
-      to_float(rw, w);
-    }
-    to_float(rx[i], v[i]);
-    if constexpr (kRes) {
-      float f[VEC];
-      to_float(rr[i], f);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] += f[j];
-      if (a.res_out != nullptr) store<VEC>(static_cast<RTs*>(a.res_out) + row * (uint64_t)H + at, v[i]);
-    }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      sum = fmaf(v[i][j], v[i][j], sum);
-      v[i][j] *= w[j];
-      most = fmaxf(most, fabsf(v[i][j]));
-    }
+    const int at = (i * (int)blockDim.x + tid) * VEC;
+    if (at >= body) continue;
+    if (NV > 1 && a.q_kind != kQuantNone) load_weights<VEC>(a, head + at, whole, w);
+    take<XT, RT, RTs, VEC>(a, row, head + at, rx[i], rr[i], w, sum, most);
   }
+  if (lone) take<XT, RT, RTs, 1>(a, row, single, lx, lr, lw, sum, most);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   most = warp_max(most);
   if (blockDim.x > 32) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
     if (lane == 0) {
       part_sum[warp] = sum;
       part_max[warp] = most;
@@ -224,53 +352,52 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormArgs a) {
   }
   const float inv = rsqrtf(sum / (float)H + a.eps);
   const float range = a.q_kind == kQuantInt8 ? 127.0f : 448.0f;
-  // Q / max|r * weight| leaves FP32 for a row of almost nothing: such values are
-  // brought up by 2^64 first (exact), a row of zeros gives zeros.
-  const float lift = most < 0x1p-60f ? 0x1p64f : 1.0f;
-  const float step = most > 0.0f ? range / (most * lift) : 0.0f;
-  if (a.q_kind != kQuantNone && threadIdx.x == 0) a.q_scale[row] = most * inv / range;
+  const Step step = code_step(most, range);
+  if (a.q_kind != kQuantNone && tid == 0) a.q_scale[row] = most * inv / range;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int at = (i * (int)blockDim.x + (int)threadIdx.x) * VEC;
-    if (at >= H) continue;
-    const uint64_t o = row * (uint64_t)H + at;
-    if (a.q_kind != kQuantNone) {
-      float f[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) f[j] = v[i][j] * lift * step;
-      store_codes<VEC>(static_cast<uint8_t*>(a.q) + o, f, a.q_kind);
-    }
-    if (a.out != nullptr) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] *= inv;
-      store<VEC>(a.out + o, v[i]);
-    }
+    const int at = (i * (int)blockDim.x + tid) * VEC;
+    if (at >= body) continue;
+    if (NV > 1) load_weights<VEC>(a, head + at, whole, w);
+    give<XT, RT, RTs, VEC>(a, row, head + at, rx[i], rr[i], w, step, inv);
   }
+  if (lone) give<XT, RT, RTs, 1>(a, row, single, lx, lr, lw, step, inv);
 }
 
 namespace {
 
-template <typename XT, typename RT, int VEC>
+template <typename XT, typename RT, int VEC, bool ENDS>
 cudaError_t launch_norm_of(const NormArgs& a, cudaStream_t stream) {
   const int pieces = (a.hidden + VEC - 1) / VEC;
-  const int nv = pieces > 2048 ? 4 : pieces > 1024 ? 2 : 1;
-  int tx = ((pieces + nv - 1) / nv + 31) / 32 * 32;
-  const int ty = tx == 32 ? 4 : 1;
-  const dim3 block(tx, ty), grid((unsigned)((a.rows + (uint32_t)ty - 1) / (uint32_t)ty));
+  auto launch = [&](auto kernel, int nv) {
+    const int tx = ((pieces + nv - 1) / nv + 31) / 32 * 32, ty = tx == 32 ? 4 : 1;
+    return launch_pdl(kernel, dim3((a.rows + (uint32_t)ty - 1) / (uint32_t)ty), dim3(tx, ty), 0, stream, a);
+  };
   if constexpr (VEC == 1) {
-    if (nv == 4 && pieces > 4096) {
-      tx = ((pieces + 31) / 32 + 31) / 32 * 32;
-      return launch_pdl(add_rms_norm_kernel<XT, RT, VEC, 32>, grid, dim3(tx, 1), 0, stream, a);
-    }
+    if (pieces > 4096) return launch(add_rms_norm_kernel<XT, RT, VEC, 32, false>, 32);
+    if (pieces > 1024) return launch(add_rms_norm_kernel<XT, RT, VEC, 4, false>, 4);
+    return launch(add_rms_norm_kernel<XT, RT, VEC, 1, false>, 1);
+  } else {
+    // Up to a row per SM, one piece per thread: the shortest way through a row
+    // (1 x 2048: 1.6 us, with two pieces 2.0).  More rows: fewer threads with more
+    // bytes each, so that more rows are on their way per SM (one, two, four pieces:
+    // 256 x 4096 BF16 3.2, 2.8, 3.6 us; 8192 x 4096 51.7, 45.0, 42.9; 8192 x 2048
+    // 25.4, 22.7, 23.5; with FP32 in and residual 88, 76, 139).
+    constexpr bool kNarrow = sizeof(XT) == 2 && !std::is_same<RT, float>::value;
+    const uint32_t sms = (uint32_t)sm_count();
+    int nv = 1;
+    if (a.rows > sms && pieces > 32) nv = kNarrow && pieces >= 512 && a.rows > 8 * sms ? 4 : 2;
+    if (pieces > 1024 * nv) nv = pieces > 2048 ? 4 : 2;
+    if (nv == 4) return launch(add_rms_norm_kernel<XT, RT, VEC, 4, ENDS>, 4);
+    if (nv == 2) return launch(add_rms_norm_kernel<XT, RT, VEC, 2, ENDS>, 2);
+    return launch(add_rms_norm_kernel<XT, RT, VEC, 1, ENDS>, 1);
   }
-  if (nv == 4) return launch_pdl(add_rms_norm_kernel<XT, RT, VEC, 4>, grid, block, 0, stream, a);
-  if (nv == 2) return launch_pdl(add_rms_norm_kernel<XT, RT, VEC, 2>, grid, block, 0, stream, a);
-  return launch_pdl(add_rms_norm_kernel<XT, RT, VEC, 1>, grid, block, 0, stream, a);
 }
 
 template <typename XT, typename RT>
 cudaError_t launch_norm_vec(const NormArgs& a, bool vec, cudaStream_t stream) {
-  return vec ? launch_norm_of<XT, RT, 8>(a, stream) : launch_norm_of<XT, RT, 1>(a, stream);
+  if (!vec) return launch_norm_of<XT, RT, 1, false>(a, stream);
+  return a.hidden % 8 == 0 ? launch_norm_of<XT, RT, 8, false>(a, stream) : launch_norm_of<XT, RT, 8, true>(a, stream);
 }
 
 template <typename XT>
@@ -299,12 +426,12 @@ cudaError_t launch_add_rms_norm(const NormConfig& c, cudaStream_t stream) {
   a.weight_f32 = c.weight_f32;
   a.q_kind = c.q != nullptr ? c.q_kind : kQuantNone;
   a.eps = c.eps;
-  // 16-byte pieces need every pointer on 16 bytes (the codes' on 8) and whole
-  // pieces per row; row strides that keep the rows there (8 BF16, 4 FP32).
-  const bool vec = c.hidden % 8 == 0 && aligned(c.x, 16) && aligned(c.residual, 16) &&
-                   aligned(c.residual_out, 16) && aligned(c.weight, 16) && aligned(c.out, 16) &&
-                   aligned(c.q, 8) && c.ldx % (c.x_f32 ? 4 : 8) == 0 &&
-                   c.ldr % (c.residual_f32 ? 4 : 8) == 0;
+  // Pieces of 8 elements need every tensor to begin on 16 bytes (the codes on 8)
+  // and every row to begin at the same place between pieces in all of them: the
+  // outputs' rows are hidden apart.
+  const bool vec = aligned(c.x, 16) && aligned(c.residual, 16) && aligned(c.residual_out, 16) &&
+                   aligned(c.weight, 16) && aligned(c.out, 16) && aligned(c.q, 8) &&
+                   c.ldx % 8 == c.hidden % 8 && (c.residual == nullptr || c.ldr % 8 == c.hidden % 8);
   return c.x_f32 ? launch_norm_res<float>(a, c.residual_f32, vec, stream)
                  : launch_norm_res<uint16_t>(a, c.residual_f32, vec, stream);
 }

@@ -127,9 +127,12 @@ NVM_DEV int4 ld_cluster_int4(uint32_t addr) {
 }
 NVM_DEV void tmap_prefetch(const void* tmap) { asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory"); }
 
-template <int BN>
+// DEEP: a ring that takes the SM, for grids of at most one CTA per SM: a stage
+// takes about 1.2 us to arrive, so the K loop's pace is that over the ring's
+// length (128 x 4096 x 4096 in 64 CTAs: 11.9 us with 4 stages of 24 KB).
+template <int BN, bool DEEP>
 struct TileCfg {
-  static constexpr int STAGES = BN == 128 ? 3 : 4;
+  static constexpr int STAGES = (BN == 128 ? 3 : 4) * (DEEP ? 2 : 1);
   static constexpr int A_BYTES = kTileM * kStageK;
   static constexpr int B_BYTES = BN * kStageK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
@@ -142,21 +145,21 @@ struct TileCfg {
   static constexpr int OFF_ABORT = OFF_TMEM + 16;
   static constexpr int SMEM = OFF_ABORT + 16 + 1024;
   static_assert(kTileM * PITCH * 4 <= OFF_SCALE && 4 * 4096 <= OFF_SCALE, "staged sums and rows fit the ring");
-  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert((DEEP ? 1 : 2) * (SMEM + 1024) <= 228 * 1024, "one or two CTAs per SM");
   // Two CTAs of this size are all an SM holds, with anything that shares it: no
   // allocation of tensor memory ever waits for another cluster's.
-  static_assert(3 * (SMEM + 1024) > 228 * 1024 && 2 * BN <= 512, "tensor memory");
+  static_assert((DEEP ? 2 : 3) * (SMEM + 1024) > 228 * 1024 && 2 * BN <= 512, "tensor memory");
 };
 
 constexpr int kTileThreads = 192;  // warp 0 loads, warp 1 issues, warps 2-5 drain
 
 }  // namespace
 
-template <int BN>
+template <int BN, bool DEEP>
 __global__ void __launch_bounds__(kTileThreads)
     int8_tile_kernel(const Int8MatmulArgs a, const uint32_t split, const __grid_constant__ CUtensorMap tm_x,
                      const __grid_constant__ CUtensorMap tm_w) {
-  using C = TileCfg<BN>;
+  using C = TileCfg<BN, DEEP>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t s_base = (raw_base + 1023u) & ~1023u;
@@ -340,10 +343,10 @@ __global__ void __launch_bounds__(kTileThreads)
 
 namespace {
 
-template <int BN>
+template <int BN, bool DEEP>
 cudaError_t launch_tile(const Int8MatmulArgs& a, uint32_t split, cudaStream_t stream) {
-  using C = TileCfg<BN>;
-  auto kern = int8_tile_kernel<BN>;
+  using C = TileCfg<BN, DEEP>;
+  auto kern = int8_tile_kernel<BN, DEEP>;
   cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM);
   if (err != cudaSuccess) return err;
   const uint64_t tiles = (uint64_t)((a.M + kTileM - 1) / kTileM) * ((a.N + BN - 1) / BN);
@@ -554,7 +557,10 @@ cudaError_t launch_int8_pair(const Int8MatmulArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_int8_tile(const Int8MatmulArgs& a, int bn, uint32_t split, cudaStream_t stream) {
-  return bn == 64 ? launch_tile<64>(a, split, stream) : launch_tile<128>(a, split, stream);
+  const uint64_t ctas = (uint64_t)((a.M + kTileM - 1) / kTileM) * ((a.N + bn - 1) / bn) * split;
+  const bool deep = ctas <= (uint64_t)sm_count();
+  if (bn == 64) return deep ? launch_tile<64, true>(a, split, stream) : launch_tile<64, false>(a, split, stream);
+  return deep ? launch_tile<128, true>(a, split, stream) : launch_tile<128, false>(a, split, stream);
 }
 
 cudaError_t read_int8_error(int* value, bool clear) { return read_error_word(&g_device_error, value, clear); }
