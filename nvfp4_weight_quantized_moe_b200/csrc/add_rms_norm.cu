@@ -191,14 +191,7 @@ NVM_DEV void load_weights(const NormArgs& a, int at, bool whole, float (&w)[VEC]
       const int s = at & 7;
       if (at - s + 16 <= a.hidden) {
         const uint4 lo = __ldg(reinterpret_cast<const uint4*>(p - s)), hi = __ldg(reinterpret_cast<const uint4*>(p - s) + 1);
-        uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-        for (int i = 0; i < 6; ++i) u[i] = s & 4 ? u[i + 2] : u[i];
-#pragma unroll
-        for (int i = 0; i < 5; ++i) u[i] = s & 2 ? u[i + 1] : u[i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = s & 1 ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
-        unpack_bf16x8(make_uint4(u[0], u[1], u[2], u[3]), w);
+        unpack_bf16x8(shift_u16x8(lo, hi, s), w);
         return;
       }
     }

@@ -124,6 +124,18 @@ NVM_DEV float activation_f32(int act, float z) {
   return silu_f32(z);
 }
 
+// Elements s .. s + 7 of the 16 16-bit elements of (lo, hi), 0 <= s < 8.
+NVM_DEV uint4 shift_u16x8(const uint4& lo, const uint4& hi, int s) {
+  uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) u[i] = s & 4 ? u[i + 2] : u[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) u[i] = s & 2 ? u[i + 1] : u[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u[i] = s & 1 ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
 // ---------------------------------------------------------------------------
 // Programmatic dependent launch and L2 prefetch
 // ---------------------------------------------------------------------------

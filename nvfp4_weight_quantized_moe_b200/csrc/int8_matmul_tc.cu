@@ -56,7 +56,8 @@ NVM_DEV void drain_rows(uint32_t taddr, int cols, uint8_t* stage, const float* w
                         const Int8MatmulArgs& a, uint32_t m0, uint32_t n0) {
   constexpr int kPer = F32 ? 4 : 8;    // outputs per piece
   constexpr int kChunk = 8 * kPer;     // columns per pass
-  const int lane = threadIdx.x & 31;
+  if (m0 >= a.M) return;  // a warp without rows
+  const int lane = threadIdx.x & 31, rows = a.M - m0 < 32u ? (int)(a.M - m0) : 32;
   const uint64_t elem = F32 ? 4 : 2;
   const bool vec = a.ldo * elem % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
 #pragma unroll 1
@@ -98,18 +99,47 @@ NVM_DEV void drain_rows(uint32_t taddr, int cols, uint8_t* stage, const float* w
       for (int i = 0; i < 8; ++i) {
         const int r = 4 * i + (lane >> 3), p = lane & 7;
         const uint4 u = *reinterpret_cast<const uint4*>(stage + r * 128 + ((p ^ (r & 7)) << 4));
-        if (m0 + r < a.M)
+        if (r < rows)
           *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + ((uint64_t)(m0 + r) * a.ldo + n0 + c0 + p * kPer) * elem) = u;
       }
     } else {
-      // An odd row distance or the last columns: single elements, lanes along the row.
-      for (int i = lane; i < 32 * kChunk; i += 32) {
-        const int r = i / kChunk, c = i % kChunk;
-        if (m0 + r < a.M && n0 + c0 + c < a.N) {
-          const uint8_t* at = stage + r * 128 + (((c / kPer) ^ (r & 7)) << 4) + (c % kPer) * elem;
-          const uint64_t o = (uint64_t)(m0 + r) * a.ldo + n0 + c0 + c;
-          if constexpr (F32) static_cast<uint32_t*>(a.out)[o] = *reinterpret_cast<const uint32_t*>(at);
-          else static_cast<uint16_t*>(a.out)[o] = *reinterpret_cast<const uint16_t*>(at);
+      // A row distance that is no whole number of pieces, or the last columns.
+      const int left = (int)(a.N - (n0 + c0) < (uint32_t)kChunk ? a.N - (n0 + c0) : kChunk);
+      if constexpr (F32) {
+        float* out = static_cast<float*>(a.out) + (uint64_t)m0 * a.ldo + n0 + c0 + lane;
+        if (lane < left) {
+#pragma unroll 8
+          for (int r = 0; r < rows; ++r, out += a.ldo)
+            *out = *reinterpret_cast<const float*>(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+        }
+      } else {
+        uint16_t* out = static_cast<uint16_t*>(a.out) + (uint64_t)m0 * a.ldo + n0 + c0;
+        auto staged = [&](int r, int p) { return *reinterpret_cast<const uint4*>(stage + r * 128 + ((p ^ (r & 7)) << 4)); };
+        auto value = [&](int r, int c) {
+          return *reinterpret_cast<const uint16_t*>(stage + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2);
+        };
+        if (left == kChunk) {
+          // `head` elements before the row's first multiple of 16 bytes, 7 pieces
+          // shifted together from the staged ones (8 where head is 0), the rest
+          // behind them: one element each for the row's 8 lanes.
+#pragma unroll 2
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), p = lane & 7;
+            if (r >= rows) continue;
+            uint16_t* row = out + (uint64_t)r * a.ldo;
+            const int head = (int)((0 - (reinterpret_cast<uintptr_t>(row) >> 1)) & 7);
+            if (p < 7 || head == 0)
+              *reinterpret_cast<uint4*>(row + head + 8 * p) = shift_u16x8(staged(r, p), staged(r, p < 7 ? p + 1 : p), head);
+            if (head != 0) {
+              const int c = p < head ? p : kChunk - 8 + p;
+              row[c] = value(r, c);
+            }
+          }
+        } else {
+          for (int i = lane; i < rows * left; i += 32) {
+            const int r = i / left, c = i % left;
+            out[(uint64_t)r * a.ldo + c] = value(r, c);
+          }
         }
       }
     }
@@ -157,8 +187,8 @@ constexpr int kTileThreads = 192;  // warp 0 loads, warp 1 issues, warps 2-5 dra
 
 template <int BN, bool DEEP>
 __global__ void __launch_bounds__(kTileThreads)
-    int8_tile_kernel(const Int8MatmulArgs a, const uint32_t split, const __grid_constant__ CUtensorMap tm_x,
-                     const __grid_constant__ CUtensorMap tm_w) {
+    int8_tile_kernel(const Int8MatmulArgs a, const uint32_t split, const uint32_t x_rows,
+                     const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w) {
   using C = TileCfg<BN, DEEP>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
@@ -217,7 +247,7 @@ __global__ void __launch_bounds__(kTileThreads)
         const uint32_t slot = i % C::STAGES, round = i / C::STAGES;
         if (round > 0 && !wait(empty + 8 * slot, (round - 1) & 1)) break;
         const uint32_t dst = s_base + slot * C::STAGE_BYTES, bar = full + 8 * slot;
-        mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
+        mbar_arrive_expect_tx(bar, x_rows * kStageK + C::B_BYTES);
         tma_load_2d(dst, &tm_x, (int)(st * kStageK), (int)m0, bar);
         tma_load_2d(dst + C::A_BYTES, &tm_w, (int)(st * kStageK), (int)n0, bar);
       }
@@ -269,10 +299,10 @@ __global__ void __launch_bounds__(kTileThreads)
           drain_rows<false>(taddr, BN, stage, scales + kTileM, scales + kTileM + BN, xs, a, m0 + 32 * q, n0);
       }
     } else {
-      // This CTA's sums, for its cluster.
+      // This CTA's sums, for its cluster (warps whose rows do not exist have none).
       int* stage = reinterpret_cast<int*>(smem) + row * C::PITCH;
 #pragma unroll 1
-      for (int c0 = 0; c0 < BN; c0 += 32) {
+      for (int c0 = m0 + 32 * q < a.M ? 0 : BN; c0 < BN; c0 += 32) {
         uint32_t d[32];
         tmem_ld32(taddr + c0, d);
         tmem_wait_ld();
@@ -288,15 +318,16 @@ __global__ void __launch_bounds__(kTileThreads)
   if (split == 1) return;
   cluster_sync();
 
-  // Rows 128 rank / split .. of the tile: the sums of all CTAs of the cluster, scaled.
-  const int rows = kTileM / (int)split;
+  // This CTA's share of the tile's rows: the sums of all CTAs of the cluster, scaled.
+  const uint32_t there = a.M - m0 < (uint32_t)kTileM ? a.M - m0 : kTileM;
+  const int rows = (int)((there + split - 1) / split);
   const int row_lo = (int)rank * rows;
   const bool vec = a.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (a.out_f32 ? 16 : 8) == 0;
 #pragma unroll 2
   for (int i = tid; i < rows * (BN / 4); i += kTileThreads) {
     const int r = row_lo + i / (BN / 4), c = i % (BN / 4) * 4;
     const uint32_t m = m0 + r, n = n0 + c;
-    if (m >= a.M || n >= a.N) continue;
+    if (r >= (int)there || n >= a.N) continue;
     const uint32_t at = s_base + (uint32_t)(r * C::PITCH + c) * 4;
     int4 s = make_int4(0, 0, 0, 0);
     for (uint32_t p = 0; p < split; ++p) {
@@ -351,15 +382,19 @@ cudaError_t launch_tile(const Int8MatmulArgs& a, uint32_t split, cudaStream_t st
   if (err != cudaSuccess) return err;
   const uint64_t tiles = (uint64_t)((a.M + kTileM - 1) / kTileM) * ((a.N + BN - 1) / BN);
   if (tiles * split > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+  // A batch of fewer than 128 tokens loads only its rows (in eights): the
+  // tile's other rows hold whatever was there, and so do their sums, which nobody
+  // reads.
+  const uint32_t x_rows = a.M < (uint32_t)kTileM ? (a.M + 7) / 8 * 8 : kTileM;
   CUtensorMap x, w;
-  err = make_map_2d_pitched(&x, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.M, a.K, a.ldx, kTileM, kStageK,
+  err = make_map_2d_pitched(&x, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.M, a.K, a.ldx, x_rows, kStageK,
                             CU_TENSOR_MAP_SWIZZLE_128B);
   if (err != cudaSuccess) return err;
   err = make_map_2d(&w, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.N, a.K, BN, kStageK, CU_TENSOR_MAP_SWIZZLE_128B);
   if (err != cudaSuccess) return err;
   const dim3 grid((unsigned)(tiles * split));
-  if (split == 1) return launch_pdl(kern, grid, dim3(kTileThreads), C::SMEM, stream, a, split, x, w);
-  return launch_pdl_cluster(kern, grid, dim3(kTileThreads), C::SMEM, split, stream, a, split, x, w);
+  if (split == 1) return launch_pdl(kern, grid, dim3(kTileThreads), C::SMEM, stream, a, split, x_rows, x, w);
+  return launch_pdl_cluster(kern, grid, dim3(kTileThreads), C::SMEM, split, stream, a, split, x_rows, x, w);
 }
 
 }  // namespace
@@ -519,7 +554,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const uint32_t dcol = tmem + lane_off + db * kPairN + half * (kPairN / 2);
-      if (ok && m0 < a.M) {
+      if (ok) {
         if (a.out_f32) drain_rows<true>(dcol, kPairN / 2, stage, scale, scale + 128, xs, a, m0, n0);
         else drain_rows<false>(dcol, kPairN / 2, stage, scale, scale + 128, xs, a, m0, n0);
       }
