@@ -16,6 +16,8 @@
 // k order inside a chunk is permuted, identically for both operands, which a sum
 // does not notice.
 
+#include <cmath>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -107,23 +109,54 @@ cudaError_t launch_reg(const Int8MatmulArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
+namespace {
+
+// Which kernel takes a product: the shortest of the estimated times below, in
+// microseconds.  Their forms follow the kernels (rounds of CTAs, a pace per
+// stage of K, bytes through the L2 at a rate, an epilogue); the numbers are a
+// fit to 178 shapes of 1 to 8192 tokens, n 64 to 16384, k 128 to 8192, measured on
+// B200 in all nine forms.  Over those shapes the choice is 1.3 % slower than the
+// best form in the geometric mean, where any single kernel is over 40 %.
+struct Form {
+  int bn;       // 0: register-fed; 64, 128: tiles of so many channels; 256: CTA pairs
+  uint32_t by;  // register-fed: 8-token tiles; tiles: CTAs that split K
+};
+
+double estimate(const Int8MatmulArgs& a, Form f, double sms) {
+  auto over = [](uint64_t x, uint64_t y) { return (double)((x + y - 1) / y); };
+  const double stages = over(a.K, 128);
+  if (f.bn == 0) {
+    const double ctas = over(a.N, 16) * over(a.M, 8 * f.by);
+    const bool one = f.by == 1;
+    return 1.1 + over(a.K, 256) * (one ? 0.29 : 0.44) + ctas * a.K * (16.0 + 8 * f.by) / (one ? 11e6 : 13e6);
+  }
+  if (f.bn == 256) return 5.1 + std::ceil(over(a.M, 256) * over(a.N, 256) / std::floor(sms / 2)) * stages * 0.39;
+  const double ctas = over(a.M, 128) * over(a.N, f.bn) * f.by, per_sm = std::ceil(ctas / sms);
+  const double own = std::ceil(stages / f.by), rows = a.M < 128 ? over(a.M, 8) * 8 : 128;
+  const double pace = own * 0.43 * (per_sm == 1 ? 1 : per_sm * 0.59);  // two CTAs of an SM overlap
+  const double bytes = ctas * own * (rows + f.bn) * 128 / 7.8e6;
+  const double tail = f.by == 1 ? per_sm * (f.bn == 64 ? 0.63 : 2.8) : 2.4 + per_sm * 0.57 * (f.bn / 64);
+  return 1.1 + (pace > bytes ? pace : bytes) + tail;
+}
+
+}  // namespace
+
 cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, cudaStream_t stream) {
-  // Up to 16 tokens the register-fed kernel, whose launch has the shortest way
-  // to its first byte (1 token, n 4096, k 2048: 4.1 us against 7.1 us on tensor
-  // cores); at 32 tokens the tiles win (n 5120, k 4096: 9.9 us against 16.6).
-  if (a.M <= 8) return launch_reg<1>(a, stream);
-  if (a.M <= 16) return launch_reg<2>(a, stream);
-  // More than 256 tokens: 256 x 256 tiles by CTA pairs (512 x 4096 x 4096: 16.5 us
-  // against 17.1 for the best split of 128 x 64 tiles, 1000 x 8192 x 4096: 29.0
-  // against 46.5).
-  if (a.M > 256) return launch_int8_pair(a, stream);
-  // Else 128 x 64 tiles with K split until two CTAs per SM are taken, at least
-  // two stages of K each.
-  const uint64_t tiles = (uint64_t)((a.M + 127) / 128) * ((a.N + 63) / 64);
-  const uint32_t nst = (a.K + 127) / 128;
-  uint32_t split = 1;
-  while (split < 8 && tiles * split * 2 <= 296 && nst >= 4 * split) split *= 2;
-  return launch_int8_tile(a, 64, split, stream);
+  static constexpr Form kForms[] = {{0, 1}, {0, 2}, {64, 1}, {64, 2}, {64, 4}, {64, 8}, {128, 1}, {128, 4}, {256, 1}};
+  const double sms = sm_count();
+  Form best = kForms[0];
+  double least = estimate(a, best, sms);
+  for (const Form& f : kForms) {
+    if (f.bn > 0 && f.by > (a.K + 127) / 128) continue;  // a stage of K for each CTA at least
+    const double t = estimate(a, f, sms);
+    if (t < least) {
+      least = t;
+      best = f;
+    }
+  }
+  if (best.bn == 0) return best.by == 1 ? launch_reg<1>(a, stream) : launch_reg<2>(a, stream);
+  if (best.bn == 256) return launch_int8_pair(a, stream);
+  return launch_int8_tile(a, best.bn, best.by, stream);
 }
 
 }  // namespace nvm

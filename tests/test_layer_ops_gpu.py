@@ -433,6 +433,31 @@ def test_matmul_larger_sizes(nvm, m, n, k):
     _check_matmul(nvm, _codes(g, m, k), _codes(g, n, k), F32, bias=torch.randn(n, generator=g, device="cuda"), seed=k)
 
 
+# Shapes that take each of the tensor-core forms (tiles of 64 and 128 channels, K
+# whole or split over 2, 4, 8 CTAs, CTA pairs), each with n a multiple of 8, even and
+# odd, batches below and above a tile's 128 rows, and k that ends inside a stage.
+FORMS = [(216, 3660, 80), (1428, 465, 96), (775, 880, 96), (64, 4711, 512), (110, 3356, 576), (79, 3696, 896),
+         (772, 1457, 544), (2331, 139, 1664), (2365, 140, 1680), (2767, 136, 1488), (3263, 1, 2512),
+         (3894, 2, 2912), (3767, 8, 2704), (49, 1870, 1472), (92, 1479, 1296), (86, 2208, 1232), (1, 1, 4480),
+         (1, 2, 4704), (2, 96, 3872), (243, 1, 4384), (203, 2, 4016), (138, 8, 4480), (26, 288, 5264),
+         (4442, 326, 784), (404, 3456, 816), (274, 4397, 992), (5, 3686, 4640), (6, 3791, 4672), (10, 3264, 3488),
+         (2866, 66, 1376), (159, 1481, 1184), (3548, 80, 1392), (2091, 2259, 96), (1794, 2708, 96), (4257, 840, 160),
+         (1025, 2305, 2064), (511, 8191, 2048)]
+
+
+@pytest.mark.parametrize("m,n,k", FORMS)
+def test_matmul_forms(nvm, m, n, k):
+    g = _gen(m * n)
+    x, w = _codes(g, m, k), _codes(g, n, k)
+    bias = torch.randn(n, generator=g, device="cuda")
+    _check_matmul(nvm, x, w, seed=1)
+    _check_matmul(nvm, x, w, bias=bias, seed=2)
+    _check_matmul(nvm, x, w, F32, seed=3)
+    _check_matmul(nvm, x, w, F32, bias=bias, seed=4)
+    _check_matmul(nvm, x, w, bias=bias, seed=5, strided=True)
+    _check_matmul(nvm, x, w, F32, seed=6, strided=True)
+
+
 @pytest.mark.parametrize("m", [1, 20, 150, 600])
 def test_matmul_strided_rows(nvm, m):
     g = _gen(m)
@@ -446,7 +471,7 @@ def test_matmul_strided_rows(nvm, m):
 @pytest.mark.parametrize("m", [1, 40, 130])
 def test_matmul_largest_sums(nvm, m):
     """All codes -128 at the longest K: the sums reach 2^31 - 2^18."""
-    k = 131056
+    k = 131056  # the limit
     x = torch.full((m, k), -128, dtype=torch.int8, device="cuda")
     w = torch.full((48, k), -128, dtype=torch.int8, device="cuda")
     w[1] = 127
