@@ -157,17 +157,21 @@ NVM_DEV int4 ld_cluster_int4(uint32_t addr) {
 }
 NVM_DEV void tmap_prefetch(const void* tmap) { asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory"); }
 
-// DEEP: a ring that takes the SM, for grids of at most one CTA per SM: a stage
-// takes about 1.2 us to arrive, so the K loop's pace is that over the ring's
-// length (128 x 4096 x 4096 in 64 CTAs: 11.9 us with 4 stages of 24 KB).
+// DEEP: a ring that takes the SM, for grids of at most one CTA per SM, with two
+// stages of K to a barrier: what bounds one CTA there is the issuing thread's way
+// from barrier to barrier, about 0.28 us, not its products (128 x 4096 x 4096 in 64
+// CTAs: 12.1 us with one stage to a barrier, 9.8 with two).  Two CTAs of an SM hide
+// each other's.
 template <int BN, bool DEEP>
 struct TileCfg {
-  static constexpr int STAGES = (BN == 128 ? 3 : 4) * (DEEP ? 2 : 1);
+  static constexpr int GROUP = DEEP ? 2 : 1;          // stages to a barrier
+  static constexpr int STAGES = BN == 128 ? 3 : 4;    // groups in the ring
   static constexpr int A_BYTES = kTileM * kStageK;
   static constexpr int B_BYTES = BN * kStageK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int GROUP_BYTES = GROUP * STAGE_BYTES;
   static constexpr int PITCH = BN + 4;  // ints between rows of the staged sums
-  static constexpr int OFF_SCALE = STAGES * STAGE_BYTES;  // floats: tokens' [128], channels' [BN], biases [BN]
+  static constexpr int OFF_SCALE = STAGES * GROUP_BYTES;  // floats: tokens' [128], channels' [BN], biases [BN]
   static constexpr int OFF_BAR = OFF_SCALE + 4 * (kTileM + 2 * BN);
   // full[STAGES], empty[STAGES], done
   static constexpr int NBAR = 2 * STAGES + 1;
@@ -243,13 +247,16 @@ __global__ void __launch_bounds__(kTileThreads)
   if (warp == 0) {
     if (lane == 0) {
       uint32_t i = 0;
-      for (uint32_t st = st_lo; st < st_hi; ++st, ++i) {
+      for (uint32_t st = st_lo; st < st_hi; st += C::GROUP, ++i) {
         const uint32_t slot = i % C::STAGES, round = i / C::STAGES;
         if (round > 0 && !wait(empty + 8 * slot, (round - 1) & 1)) break;
-        const uint32_t dst = s_base + slot * C::STAGE_BYTES, bar = full + 8 * slot;
-        mbar_arrive_expect_tx(bar, x_rows * kStageK + C::B_BYTES);
-        tma_load_2d(dst, &tm_x, (int)(st * kStageK), (int)m0, bar);
-        tma_load_2d(dst + C::A_BYTES, &tm_w, (int)(st * kStageK), (int)n0, bar);
+        const uint32_t bar = full + 8 * slot, n = min((uint32_t)C::GROUP, st_hi - st);
+        mbar_arrive_expect_tx(bar, n * (x_rows * kStageK + C::B_BYTES));
+        for (uint32_t g = 0; g < n; ++g) {
+          const uint32_t dst = s_base + slot * C::GROUP_BYTES + g * C::STAGE_BYTES;
+          tma_load_2d(dst, &tm_x, (int)((st + g) * kStageK), (int)m0, bar);
+          tma_load_2d(dst + C::A_BYTES, &tm_w, (int)((st + g) * kStageK), (int)n0, bar);
+        }
       }
       // Nothing may still land in this CTA's memory when it goes on.
       for (uint32_t j = i > (uint32_t)C::STAGES ? i - C::STAGES : 0; j < i; ++j)
@@ -260,15 +267,19 @@ __global__ void __launch_bounds__(kTileThreads)
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_s8_s32(kTileM, BN);
       uint32_t i = 0;
-      for (uint32_t st = st_lo; st < st_hi; ++st, ++i) {
+      for (uint32_t st = st_lo; st < st_hi; st += C::GROUP, ++i) {
         const uint32_t slot = i % C::STAGES;
         if (!wait(full + 8 * slot, (i / C::STAGES) & 1)) break;
         tc_fence_after();
-        const uint32_t abase = s_base + slot * C::STAGE_BYTES, bbase = abase + C::A_BYTES;
 #pragma unroll
-        for (int k = 0; k < kStageK / 32; ++k)
-          tc_mma_s8_ss(tmem, smem_desc_sw128(abase + 32 * k), smem_desc_sw128(bbase + 32 * k), idesc,
-                       i > 0 || k > 0 ? 1u : 0u);
+        for (int g = 0; g < C::GROUP; ++g) {
+          if (st + g >= st_hi) break;
+          const uint32_t abase = s_base + slot * C::GROUP_BYTES + g * C::STAGE_BYTES, bbase = abase + C::A_BYTES;
+#pragma unroll
+          for (int k = 0; k < kStageK / 32; ++k)
+            tc_mma_s8_ss(tmem, smem_desc_sw128(abase + 32 * k), smem_desc_sw128(bbase + 32 * k), idesc,
+                         i > 0 || g > 0 || k > 0 ? 1u : 0u);
+        }
         tc_commit(empty + 8 * slot);
       }
       tc_commit(done);
