@@ -84,6 +84,19 @@ NVM_DEV F warp_sum(F v) {
 
 constexpr int kMaxWarps = 4;
 
+// 2^x and 1 / x as the hardware has them (2^-22 off, results below the normal
+// range 0), for scores that are only compared.
+NVM_DEV float exp2_near(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+NVM_DEV float recip_near(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 struct RouteArgs {
   const void* logits;
   const float* bias;
@@ -313,13 +326,15 @@ NVM_DEV void select_experts(const RouteArgs& a, const T* row, const float (&l)[E
   const int lane = threadIdx.x & 31, e0 = lane * a.per_lane;
   const bool scored = a.bias != nullptr;  // the choice is s + bias; else the logit
   // Error of an FP32 s.  Sigmoid: the exponential is off by (2 + 1.2 |x|) 2^-23 of
-  // its value, which s (1 - s) weighs to under 2^-23; 1 + exp and the quotient add
-  // 2^-24 and 2^-22: under 2^-21.  Softmax, in units of the largest score 1 / sum:
+  // its value (its own error, and the rounded product in its exponent), which
+  // s (1 - s) weighs to under 2^-23; 1 + exp and the quotient add 2^-24 and 2^-23:
+  // under 2^-21.  Softmax, in units of the largest score 1 / sum:
   // the difference and the exponential as much, the sum EPL + 5 roundings.  s + bias
   // adds 2^-24 of its value.  Twice that for two neighbours.
   const float unit = a.softmax ? zinv * (8 + 2 * (EPL + 5)) * 0x1p-23f : 0x1p-20f;
   auto bound = [&](float v) { return unit + fabsf(v) * 0x1p-23f; };
-  auto score = [&](float x) { return a.softmax ? __expf(x - lmax) * zinv : __fdividef(1.0f, 1.0f + __expf(-x)); };
+  auto softmax_score = [&](float x) { return exp2_near((x - lmax) * 1.44269504f) * zinv; };
+  auto sigmoid_score = [&](float x) { return recip_near(1.0f + exp2_near(x * -1.44269504f)); };
 
   uint32_t key[EPL];
   if (scored) {
@@ -339,8 +354,12 @@ NVM_DEV void select_experts(const RouteArgs& a, const T* row, const float (&l)[E
 #pragma unroll
       for (int j = 0; j < EPL; ++j) b[j] = j < a.per_lane && e0 + j < a.E ? __ldg(a.bias + e0 + j) : 0.0f;
     }
+    auto choose = [&](auto score) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) key[j] = l[j] == -INFINITY ? 0 : order_key(or_minus_infinity(score(l[j]) + b[j]));
+      for (int j = 0; j < EPL; ++j) key[j] = l[j] == -INFINITY ? 0 : order_key(or_minus_infinity(score(l[j]) + b[j]));
+    };
+    if (a.softmax) choose(softmax_score);
+    else choose(sigmoid_score);
   } else {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) key[j] = order_key(l[j]);
@@ -349,9 +368,15 @@ NVM_DEV void select_experts(const RouteArgs& a, const T* row, const float (&l)[E
   unsigned mask = 1u;
   if (a.groups > 1) {
     const bool sums = a.group_top > 1;
-    const uint32_t mine = group_scores<float, EPL>(a, [&](int j) -> uint32_t {
-      return scored || !sums || key[j] <= kNone ? key[j] : order_key(score(l[j]));
-    });
+    uint32_t mine;
+    if (scored || !sums) {
+      mine = group_scores<float, EPL>(a, [&](int j) -> uint32_t { return key[j]; });
+    } else {
+      mine = group_scores<float, EPL>(a, [&](int j) -> uint32_t {
+        if (key[j] <= kNone) return 0;
+        return order_key(a.softmax ? softmax_score(l[j]) : sigmoid_score(l[j]));
+      });
+    }
     mask = best_groups(a, mine, kNone);
     if (scored || sums) {
       // The worst kept against the best left out (there may be none).
@@ -364,10 +389,14 @@ NVM_DEV void select_experts(const RouteArgs& a, const T* row, const float (&l)[E
           mask = groups_exactly<T, EPL>(a, row, scores_exactly<T>(a, row, lmax));
       }
     }
+    if (a.group_lanes > 0) {
+      const uint32_t stays = (mask >> (lane / a.group_lanes)) & 1u ? 0xffffffffu : 0u;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const bool stays = a.group_lanes > 0 ? ((mask >> (lane / a.group_lanes)) & 1u) != 0 : in_mask(a, mask, e0 + j);
-      if (!stays) key[j] = 0;
+      for (int j = 0; j < EPL; ++j) key[j] &= stays;
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if (!in_mask(a, mask, e0 + j)) key[j] = 0;
     }
   }
 
