@@ -26,6 +26,12 @@ if not os.path.exists(LIB_PATH):
         "(nvcc, sm_100a). There is no CPU fallback.")
 
 _lib = ctypes.CDLL(LIB_PATH)
+try:
+    from . import _quick_call
+except ImportError as e:
+    raise ImportError(
+        f"the binding's C++ part does not load ({e}): build it with "
+        "`python nvfp4_weight_quantized_moe_b200/build.py` against the installed PyTorch") from e
 
 c_void_p = ctypes.c_void_p
 c_u32 = ctypes.c_uint32
@@ -457,17 +463,17 @@ def forward_nongated(x, topk_ids, topk_weights, up: ExpertTables, down: ExpertTa
 
 # --- the operators around the forward ------------------------------------------
 # Their rows may be strided views, and they run on the device of their tensors,
-# on that device's current stream unless one is given.  Their arguments go over
-# as one packed struct (the library reads it during the call): a decode step
-# makes these calls in microseconds, and ctypes takes 0.1 us per argument.  Each
-# call tests its tensors in one expression of cheap attributes; only if that fails
-# does it look for what is wrong (or for what the expression does not know).
+# on that device's current stream unless one is given.  The usual call (contiguous
+# tensors on the current device and its stream) goes through _quick_call, which
+# checks the tensors in C++; it returns -1 where something is different, and the
+# code here then finds strides and devices, or says what is wrong.  Arguments go
+# over as one packed struct, which the library reads during the call.
 
 _ROUTE_ARGS = struct.Struct("PPPPQIIIIIIiiif")   # nvfp4_moe_route_args
 _NORM_ARGS = struct.Struct("PPPPPPPQQIIiiiif")   # nvfp4_moe_norm_args
 _INT8_ARGS = struct.Struct("PPPPPPQQIIIi")       # nvfp4_moe_int8_args
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+_quick_call.bind(*(ctypes.cast(getattr(_lib, f), c_void_p).value for f in (
+    "nvfp4_moe_route_topk", "nvfp4_moe_add_rms_norm", "nvfp4_moe_int8_matmul")))
 
 
 def _rows(t: torch.Tensor, name: str):
@@ -484,24 +490,18 @@ def _on(t: torch.Tensor, dev: int, name: str, dtype=None) -> int:
     """The tensor's address, after checking its device and type."""
     if t.get_device() != dev:  # -1 on the CPU
         raise ValueError(f"{name}: must be a CUDA tensor on the same device as the others")
-    if dtype is not None and t.dtype is not dtype:
+    if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     return t.data_ptr()
 
 
 def _vector(t: torch.Tensor, n: int, dev: int, name: str, dtype=torch.float32) -> int:
-    if (t.ndim == 1 and t.numel() == n and t.is_contiguous() and t.get_device() == dev
-            and (dtype is None or t.dtype is dtype)):
-        return t.data_ptr()
-    if t.ndim != 1 or t.numel() != n or not t.is_contiguous():
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name}: must be a contiguous vector of {n} values")
     return _on(t, dev, name, dtype)
 
 
 def _matrix(t: torch.Tensor, m: int, n: int, dev: int, name: str, dtype=None) -> int:
-    if (t.shape == (m, n) and t.is_contiguous() and t.get_device() == dev
-            and (dtype is None or t.dtype is dtype)):
-        return t.data_ptr()
     if t.shape != (m, n) or not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous [{m}, {n}]")
     return _on(t, dev, name, dtype)
@@ -520,20 +520,14 @@ def _cuda_device(t: torch.Tensor, name: str) -> int:
     return t.get_device()
 
 
-def _launch(name: str, fn, layout: struct.Struct, fields, dev: int, stream) -> None:
+def _launch(name: str, layout: struct.Struct, fields, dev: int, stream) -> None:
     """Call the entry point with the tensors' device current."""
     try:
         args = layout.pack(*fields)
     except (struct.error, OverflowError) as e:
         raise ValueError(f"{name}: argument out of range ({e})") from None
-    stream = _current_stream(dev) if stream is None else _stream(stream)
-    if _current_device() == dev:
-        status = fn(args, stream)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(args, stream)
-    if status != 0:
-        raise NVFP4MoEError(name, status)
+    with torch.cuda.device(dev):
+        _check(name, getattr(_lib, name)(args, _stream(stream)))
 
 
 def route_topk(logits, topk_ids, topk_weights, *, score="softmax", bias=None, num_groups=1,
@@ -549,24 +543,20 @@ def route_topk(logits, topk_ids, topk_weights, *, score="softmax", bias=None, nu
     code = SCORES.get(score)
     if code is None:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
-    dev, kind, shape, out = logits.get_device(), _FLOAT_TYPES.get(logits.dtype), logits.shape, topk_ids.shape
-    if (dev >= 0 and kind is not None and len(shape) == len(out) == 2 and out[0] == shape[0]
-            and logits.is_contiguous() and topk_weights.shape == out
-            and topk_ids.dtype is torch.int32 and topk_weights.dtype is torch.float32
-            and topk_ids.is_contiguous() and topk_weights.is_contiguous()
-            and topk_ids.get_device() == dev and topk_weights.get_device() == dev):
-        m, e = shape
-        k, ld, ids, weights = out[1], e, topk_ids.data_ptr(), topk_weights.data_ptr()
-    else:
-        dev, kind = _cuda_device(logits, "logits"), _type_code(logits, "logits")
-        m, e, ld = _rows(logits, "logits")
-        if len(out) != 2:
-            raise ValueError("topk_ids: must be [M, topk]")
-        k = out[1]
-        ids = _matrix(topk_ids, m, k, dev, "topk_ids", torch.int32)
-        weights = _matrix(topk_weights, m, k, dev, "topk_weights", torch.float32)
+    if stream is None:
+        status = _quick_call.route_topk(logits, topk_ids, topk_weights, bias, code, num_groups, topk_groups,
+                                        group_top, renormalize, scale)
+        if status >= 0:
+            return _check("nvfp4_moe_route_topk", status)
+    dev, kind = _cuda_device(logits, "logits"), _type_code(logits, "logits")
+    m, e, ld = _rows(logits, "logits")
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids: must be [M, topk]")
+    k = topk_ids.shape[1]
+    ids = _matrix(topk_ids, m, k, dev, "topk_ids", torch.int32)
+    weights = _matrix(topk_weights, m, k, dev, "topk_weights", torch.float32)
     b = 0 if bias is None else _vector(bias, e, dev, "bias")
-    _launch("nvfp4_moe_route_topk", _lib.nvfp4_moe_route_topk, _ROUTE_ARGS,
+    _launch("nvfp4_moe_route_topk", _ROUTE_ARGS,
             (logits.data_ptr(), b, ids, weights, ld, m, e, k, num_groups, topk_groups, group_top,
              kind, code, 1 if renormalize else 0, scale), dev, stream)
 
@@ -580,25 +570,21 @@ def add_rms_norm(x, weight, eps, *, out=None, residual=None, residual_out=None, 
     residual's type), ``out`` (y in bf16), ``q`` with ``q_scale`` (y in int8 or
     float8_e4m3fn codes, one f32 scale per row).  ``residual_out`` may be
     ``residual`` itself."""
-    dev, kind, shape = x.get_device(), _FLOAT_TYPES.get(x.dtype), x.shape
-    if dev >= 0 and kind is not None and len(shape) == 2 and x.is_contiguous():
-        m, h = shape
-        ldx = h
-    else:
-        dev, kind = _cuda_device(x, "x"), _type_code(x, "x")
-        m, h, ldx = _rows(x, "x")
+    if stream is None:
+        status = _quick_call.add_rms_norm(x, weight, eps, out, residual, residual_out, q, q_scale)
+        if status >= 0:
+            return _check("nvfp4_moe_add_rms_norm", status)
+    dev, kind = _cuda_device(x, "x"), _type_code(x, "x")
+    m, h, ldx = _rows(x, "x")
     w_kind = _type_code(weight, "weight")
     w = _vector(weight, h, dev, "weight", None)
     r = r_out = r_kind = ldr = y = codes = scales = q_kind = 0
     if residual is not None:
         r_kind = _type_code(residual, "residual")
-        if residual.shape == shape and residual.get_device() == dev and residual.is_contiguous():
-            r, ldr = residual.data_ptr(), h
-        else:
-            rm, rh, ldr = _rows(residual, "residual")
-            if (rm, rh) != (m, h):
-                raise ValueError("residual: must have the shape of x")
-            r = _on(residual, dev, "residual")
+        rm, rh, ldr = _rows(residual, "residual")
+        if (rm, rh) != (m, h):
+            raise ValueError("residual: must have the shape of x")
+        r = _on(residual, dev, "residual")
     if residual_out is not None:
         if residual is None:
             raise ValueError("residual_out given without residual")
@@ -611,7 +597,7 @@ def add_rms_norm(x, weight, eps, *, out=None, residual=None, residual_out=None, 
         q_kind = _type_code(q, "q", _CODE_TYPES)
         codes = _matrix(q, m, h, dev, "q")
         scales = _vector(q_scale, m, dev, "q_scale")
-    _launch("nvfp4_moe_add_rms_norm", _lib.nvfp4_moe_add_rms_norm, _NORM_ARGS,
+    _launch("nvfp4_moe_add_rms_norm", _NORM_ARGS,
             (x.data_ptr(), r, r_out, w, y, codes, scales, ldx, ldr, m, h, kind, r_kind, w_kind, q_kind,
              eps), dev, stream)
 
@@ -621,35 +607,22 @@ def int8_matmul(x_q, x_scale, w_q, w_scale, out, *, bias=None, stream=None) -> N
     ``x_q`` int8 [M, K] (rows may be strided), ``w_q`` int8 [N, K], f32 scales [M] and
     [N], f32 ``bias`` [N] or None, ``out`` bf16 or f32 [M, N] (rows may be strided).
     K is a multiple of 16; the integer sums are exact."""
-    dev, kind, shape, w_shape, i8, f32 = (x_q.get_device(), _FLOAT_TYPES.get(out.dtype), x_q.shape,
-                                          w_q.shape, torch.int8, torch.float32)
-    if (dev >= 0 and kind is not None and len(shape) == len(w_shape) == 2 and w_shape[1] == shape[1]
-            and out.shape == (shape[0], w_shape[0]) and x_scale.ndim == 1 and w_scale.ndim == 1
-            and x_scale.numel() == shape[0] and w_scale.numel() == w_shape[0]
-            and x_q.dtype is i8 and w_q.dtype is i8
-            and x_scale.dtype is f32 and w_scale.dtype is f32
-            and w_q.get_device() == dev and out.get_device() == dev
-            and x_scale.get_device() == dev and w_scale.get_device() == dev
-            and x_q.is_contiguous() and w_q.is_contiguous() and out.is_contiguous()
-            and x_scale.is_contiguous() and w_scale.is_contiguous()):
-        m, k = shape
-        n = w_shape[0]
-        ldx, ldo = k, n
-    else:
-        dev, kind = _cuda_device(x_q, "x_q"), _type_code(out, "out")
-        m, k, ldx = _rows(x_q, "x_q")
-        if len(w_shape) != 2:
-            raise ValueError("w_q: must be [N, K]")
-        n = w_shape[0]
-        _on(x_q, dev, "x_q", i8)
-        _matrix(w_q, n, k, dev, "w_q", i8)
-        _vector(x_scale, m, dev, "x_scale")
-        _vector(w_scale, n, dev, "w_scale")
-        om, on, ldo = _rows(out, "out")
-        if (om, on) != (m, n):
-            raise ValueError(f"out: must be [{m}, {n}]")
-        _on(out, dev, "out")
+    if stream is None:
+        status = _quick_call.int8_matmul(x_q, x_scale, w_q, w_scale, out, bias)
+        if status >= 0:
+            return _check("nvfp4_moe_int8_matmul", status)
+    dev, kind = _cuda_device(x_q, "x_q"), _type_code(out, "out")
+    m, k, ldx = _rows(x_q, "x_q")
+    x = _on(x_q, dev, "x_q", torch.int8)
+    if w_q.dim() != 2:
+        raise ValueError("w_q: must be [N, K]")
+    n = w_q.shape[0]
+    w = _matrix(w_q, n, k, dev, "w_q", torch.int8)
+    xs = _vector(x_scale, m, dev, "x_scale")
+    ws = _vector(w_scale, n, dev, "w_scale")
+    om, on, ldo = _rows(out, "out")
+    if (om, on) != (m, n):
+        raise ValueError(f"out: must be [{m}, {n}]")
     b = 0 if bias is None else _vector(bias, n, dev, "bias")
-    _launch("nvfp4_moe_int8_matmul", _lib.nvfp4_moe_int8_matmul, _INT8_ARGS,
-            (x_q.data_ptr(), x_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), b,
-             out.data_ptr(), ldx, ldo, m, n, k, kind), dev, stream)
+    _launch("nvfp4_moe_int8_matmul", _INT8_ARGS,
+            (x, xs, w, ws, b, _on(out, dev, "out"), ldx, ldo, m, n, k, kind), dev, stream)

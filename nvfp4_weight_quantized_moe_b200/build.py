@@ -1,4 +1,5 @@
-"""Build the sm_100a shared library ``libnvfp4moe.so`` in-tree with nvcc.
+"""Build the sm_100a shared library ``libnvfp4moe.so`` in-tree with nvcc, and the
+binding's small C++ part (``_quick_call``, against the installed PyTorch) with g++.
 
     python nvfp4_weight_quantized_moe_b200/build.py [--verbose-ptxas] [--force]
 
@@ -16,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -23,6 +25,9 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libnvfp4moe.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
+
+QUICK_SRC = os.path.join(CSRC, "quick_call.cpp")
+QUICK_PATH = os.path.join(PKG_DIR, "_quick_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -47,7 +52,30 @@ def needs_build() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_quick_call(force: bool = False) -> str:
+    """The binding's C++ part: the tensors' checks and the call without ctypes."""
+    deps = [QUICK_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(QUICK_PATH) and all(
+            os.path.getmtime(d) <= os.path.getmtime(QUICK_PATH) for d in deps):
+        return QUICK_PATH
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(cuda, "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE, "-o", QUICK_PATH + ".tmp", QUICK_SRC,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError(f"g++ failed with exit code {res.returncode}")
+    os.replace(QUICK_PATH + ".tmp", QUICK_PATH)
+    return QUICK_PATH
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    build_quick_call(force)
     if not force and not verbose_ptxas and not needs_build():
         return LIB_PATH
     cmd = [
