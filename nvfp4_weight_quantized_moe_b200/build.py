@@ -79,7 +79,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and not verbose_ptxas and not needs_build():
         return LIB_PATH
     cmd = [
-        nvcc_path(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "--shared",
+        nvcc_path(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "--shared", "--threads", "0",
         "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC,
         "-DNVFP4_MOE_BUILD", "-o", LIB_PATH + ".tmp",
     ]

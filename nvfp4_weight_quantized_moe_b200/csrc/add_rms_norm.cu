@@ -10,9 +10,10 @@
 // y: the residual's rounding to BF16 does not enter the norm.  Since y is
 // r * weight times one factor per row, q = r * weight * (Q / max|r * weight|):
 // max and mean square are reduced together, in one pass over a row that stays in
-// registers.  The product and the quotient keep their rounding errors until q is
-// rounded, so a code goes to the other neighbour less often than with the
-// division as written.
+// registers.  Roundings before a code's: r, the product, the quotient of the row
+// and its product, as many as in dividing y by the scale; keeping the errors until
+// the code is formed costs 2 us of 4 at 256 x 7168 (60 operations an element instead
+// of 25) and moves one code in two million.
 //
 // Bound by HBM: each input is read once, each output written once (8192 x 4096
 // BF16 with residual: 42.9 us, 96 % of the copy bandwidth).  A row belongs to one
@@ -128,24 +129,43 @@ NVM_DEV uint32_t e4m3x2_bits(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// To int8, nearest even, within +-127; NaN gives 0.
-NVM_DEV uint32_t int8_bits(float v) { return (uint32_t)__float2int_rn(fminf(fmaxf(v, -127.0f), 127.0f)) & 0xffu; }
 
+// What turns r * weight into the value that its code is nearest to: Q / the largest
+// |r * weight|.  Values below 2^-60, whose quotient would leave FP32, are brought
+// up by `lift` first (exact); a row of zeros gives zeros.
+struct Step {
+  float lift, step;
+};
+NVM_DEV Step code_step(float most, float range) {
+  Step s{most < 0x1p-60f ? 0x1p64f : 1.0f, 0.0f};
+  if (most > 0.0f) s.step = range / (most * s.lift);
+  return s;
+}
+
+// Codes of VEC values.
 template <int VEC>
 NVM_DEV void store_codes(uint8_t* p, const float (&f)[VEC], int kind) {
-  if constexpr (VEC == 8) {
-    uint2 u;
-    if (kind == kQuantInt8) {
-      u.x = int8_bits(f[0]) | int8_bits(f[1]) << 8 | int8_bits(f[2]) << 16 | int8_bits(f[3]) << 24;
-      u.y = int8_bits(f[4]) | int8_bits(f[5]) << 8 | int8_bits(f[6]) << 16 | int8_bits(f[7]) << 24;
+  uint32_t word[(VEC + 3) / 4];
+  if (kind == kQuantInt8) {
+    // Adding 1.5 * 2^23 rounds to a whole number, whose low byte is the code.
+    uint32_t c[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) c[j] = __float_as_uint(f[j] + 12582912.0f);
+    if constexpr (VEC == 1) {
+      word[0] = c[0];
     } else {
-      u.x = e4m3x2_bits(f[0], f[1]) | e4m3x2_bits(f[2], f[3]) << 16;
-      u.y = e4m3x2_bits(f[4], f[5]) | e4m3x2_bits(f[6], f[7]) << 16;
+#pragma unroll
+      for (int j = 0; j < VEC; j += 4)
+        word[j / 4] = __byte_perm(__byte_perm(c[j], c[j + 1], 0x0040), __byte_perm(c[j + 2], c[j + 3], 0x0040), 0x5410);
     }
-    *reinterpret_cast<uint2*>(p) = u;
+  } else if constexpr (VEC == 1) {
+    word[0] = e4m3x2_bits(f[0], 0.0f);
   } else {
-    *p = (uint8_t)(kind == kQuantInt8 ? int8_bits(f[0]) : e4m3x2_bits(f[0], 0.0f) & 0xffu);
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4) word[j / 4] = e4m3x2_bits(f[j], f[j + 1]) | e4m3x2_bits(f[j + 2], f[j + 3]) << 16;
   }
+  if constexpr (VEC == 8) *reinterpret_cast<uint2*>(p) = make_uint2(word[0], word[1]);
+  else *p = (uint8_t)word[0];
 }
 
 // VEC weights from `at` on.  Not `whole`: between pieces, so the pieces on either
@@ -213,8 +233,8 @@ NVM_DEV void add(const Raw<XT, VEC>& rx, const Raw<RTs, VEC>& rr, float (&r)[VEC
 }
 
 // First pass over VEC elements: r to residual_out, its squares into `sum` and,
-// for codes, the largest r * weight into `most`.
-template <typename XT, typename RT, typename RTs, int VEC>
+// for codes, the largest |r * weight| into `most`.
+template <typename XT, typename RT, typename RTs, int VEC, bool CODES>
 NVM_DEV void take(const NormArgs& a, uint64_t row, int at, const Raw<XT, VEC>& rx, const Raw<RTs, VEC>& rr,
                   const float (&w)[VEC], float& sum, float& most) {
   float r[VEC];
@@ -223,46 +243,30 @@ NVM_DEV void take(const NormArgs& a, uint64_t row, int at, const Raw<XT, VEC>& r
     store<VEC>(static_cast<RTs*>(a.res_out) + row * (uint64_t)a.hidden + at, r);
 #pragma unroll
   for (int j = 0; j < VEC; ++j) sum = fmaf(r[j], r[j], sum);
-  if (a.q_kind != kQuantNone) {
+  if constexpr (CODES) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) most = fmaxf(most, fabsf(r[j] * w[j]));
   }
 }
 
-// Q / max|r * weight| as hi + lo; values below 2^-60, whose quotient would leave
-// FP32, are brought up by `lift` first (exact).  A row of zeros gives zeros.
-struct Step {
-  float lift, hi, lo;
-};
-NVM_DEV Step code_step(float most, float range) {
-  Step s{most < 0x1p-60f ? 0x1p64f : 1.0f, 0.0f, 0.0f};
-  if (most > 0.0f) {
-    const float m = most * s.lift;
-    s.hi = range / m;
-    const float lo = fmaf(-s.hi, m, range) / m;
-    s.lo = fabsf(lo) < INFINITY ? lo : 0.0f;  // not of an infinite row
-  }
-  return s;
-}
-
 // Second pass: the codes and the norm.
-template <typename XT, typename RT, typename RTs, int VEC>
+template <typename XT, typename RT, typename RTs, int VEC, bool CODES>
 NVM_DEV void give(const NormArgs& a, uint64_t row, int at, const Raw<XT, VEC>& rx, const Raw<RTs, VEC>& rr,
                   const float (&w)[VEC], const Step& step, float inv) {
   const uint64_t o = row * (uint64_t)a.hidden + at;
-  float r[VEC], f[VEC];
+  float r[VEC];
   add<XT, RT>(rx, rr, r);
-  if (a.q_kind != kQuantNone) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float t = r[j] * w[j], off = fmaf(r[j], w[j], -t);  // t + off is the product
-      f[j] = fmaf(t * step.lift, step.hi, fmaf(t * step.lift, step.lo, off * step.lift * step.hi));
-    }
-    store_codes<VEC>(static_cast<uint8_t*>(a.q) + o, f, a.q_kind);
+  for (int j = 0; j < VEC; ++j) r[j] *= w[j];
+  if constexpr (CODES) {
+    float c[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) c[j] = r[j] * step.lift * step.step;
+    store_codes<VEC>(static_cast<uint8_t*>(a.q) + o, c, a.q_kind);
   }
   if (a.out != nullptr) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) r[j] = r[j] * w[j] * inv;
+    for (int j = 0; j < VEC; ++j) r[j] *= inv;
     store<VEC>(a.out + o, r);
   }
 }
@@ -276,11 +280,12 @@ NVM_DEV void give(const NormArgs& a, uint64_t row, int at, const Raw<XT, VEC>& r
 // their way.  Pieces of 8 lie on multiples of 8 elements of the tensors; with ENDS
 // a row that does not begin or end on one has up to 7 single elements at either
 // end, one each for the first threads.
-template <typename XT, typename RT, int VEC, int NV, bool ENDS>
+template <typename XT, typename RT, int VEC, int NV, bool ENDS, bool CODES>
 __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormArgs a) {
   constexpr bool kRes = !std::is_same<RT, NoResidual>::value;
   using RTs = typename std::conditional<kRes, RT, uint16_t>::type;
-  __shared__ float part_sum[32], part_max[32];
+  __shared__ float part_sum[32];
+  __shared__ float part_most[32];
   griddep_wait();
   griddep_launch_dependents();
   const uint64_t row = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -318,48 +323,48 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormArgs a) {
   // One piece per thread: its weights come with it.
   if (NV == 1 && tid * VEC < body) load_weights<VEC>(a, head + tid * VEC, whole, w);
 
-  float sum = 0.0f, most = 0.0f;
+  float sum = 0.0f;
+  float most = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int at = (i * (int)blockDim.x + tid) * VEC;
     if (at >= body) continue;
-    if (NV > 1 && a.q_kind != kQuantNone) load_weights<VEC>(a, head + at, whole, w);
-    take<XT, RT, RTs, VEC>(a, row, head + at, rx[i], rr[i], w, sum, most);
+    if (NV > 1 && CODES) load_weights<VEC>(a, head + at, whole, w);
+    take<XT, RT, RTs, VEC, CODES>(a, row, head + at, rx[i], rr[i], w, sum, most);
   }
-  if (lone) take<XT, RT, RTs, 1>(a, row, single, lx, lr, lw, sum, most);
+  if (lone) take<XT, RT, RTs, 1, CODES>(a, row, single, lx, lr, lw, sum, most);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  most = warp_max(most);
+  if constexpr (CODES) most = warp_max(most);
   if (blockDim.x > 32) {
     const int warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
     if (lane == 0) {
       part_sum[warp] = sum;
-      part_max[warp] = most;
+      if constexpr (CODES) part_most[warp] = most;
     }
     __syncthreads();
     sum = lane < warps ? part_sum[lane] : 0.0f;
-    most = lane < warps ? part_max[lane] : 0.0f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    most = warp_max(most);
+    if constexpr (CODES) most = warp_max(lane < warps ? part_most[lane] : 0.0f);
   }
   const float inv = rsqrtf(sum / (float)H + a.eps);
   const float range = a.q_kind == kQuantInt8 ? 127.0f : 448.0f;
   const Step step = code_step(most, range);
-  if (a.q_kind != kQuantNone && tid == 0) a.q_scale[row] = most * inv / range;
+  if (CODES && tid == 0) a.q_scale[row] = most * inv / range;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int at = (i * (int)blockDim.x + tid) * VEC;
     if (at >= body) continue;
     if (NV > 1) load_weights<VEC>(a, head + at, whole, w);
-    give<XT, RT, RTs, VEC>(a, row, head + at, rx[i], rr[i], w, step, inv);
+    give<XT, RT, RTs, VEC, CODES>(a, row, head + at, rx[i], rr[i], w, step, inv);
   }
-  if (lone) give<XT, RT, RTs, 1>(a, row, single, lx, lr, lw, step, inv);
+  if (lone) give<XT, RT, RTs, 1, CODES>(a, row, single, lx, lr, lw, step, inv);
 }
 
 namespace {
 
-template <typename XT, typename RT, int VEC, bool ENDS>
+template <typename XT, typename RT, int VEC, bool ENDS, bool CODES>
 cudaError_t launch_norm_of(const NormArgs& a, cudaStream_t stream) {
   const int pieces = (a.hidden + VEC - 1) / VEC;
   auto launch = [&](auto kernel, int nv) {
@@ -367,9 +372,9 @@ cudaError_t launch_norm_of(const NormArgs& a, cudaStream_t stream) {
     return launch_pdl(kernel, dim3((a.rows + (uint32_t)ty - 1) / (uint32_t)ty), dim3(tx, ty), 0, stream, a);
   };
   if constexpr (VEC == 1) {
-    if (pieces > 4096) return launch(add_rms_norm_kernel<XT, RT, VEC, 32, false>, 32);
-    if (pieces > 1024) return launch(add_rms_norm_kernel<XT, RT, VEC, 4, false>, 4);
-    return launch(add_rms_norm_kernel<XT, RT, VEC, 1, false>, 1);
+    if (pieces > 4096) return launch(add_rms_norm_kernel<XT, RT, VEC, 32, false, CODES>, 32);
+    if (pieces > 1024) return launch(add_rms_norm_kernel<XT, RT, VEC, 4, false, CODES>, 4);
+    return launch(add_rms_norm_kernel<XT, RT, VEC, 1, false, CODES>, 1);
   } else {
     // Up to a row per SM, one piece per thread: the shortest way through a row
     // (1 x 2048: 1.6 us, with two pieces 2.0).  More rows: fewer threads with more
@@ -381,22 +386,29 @@ cudaError_t launch_norm_of(const NormArgs& a, cudaStream_t stream) {
     int nv = 1;
     if (a.rows > sms && pieces > 32) nv = kNarrow && pieces >= 512 && a.rows > 8 * sms ? 4 : 2;
     if (pieces > 1024 * nv) nv = pieces > 2048 ? 4 : 2;
-    if (nv == 4) return launch(add_rms_norm_kernel<XT, RT, VEC, 4, ENDS>, 4);
-    if (nv == 2) return launch(add_rms_norm_kernel<XT, RT, VEC, 2, ENDS>, 2);
-    return launch(add_rms_norm_kernel<XT, RT, VEC, 1, ENDS>, 1);
+    if (nv == 4) return launch(add_rms_norm_kernel<XT, RT, VEC, 4, ENDS, CODES>, 4);
+    if (nv == 2) return launch(add_rms_norm_kernel<XT, RT, VEC, 2, ENDS, CODES>, 2);
+    return launch(add_rms_norm_kernel<XT, RT, VEC, 1, ENDS, CODES>, 1);
   }
 }
 
-template <typename XT, typename RT>
+template <typename XT, typename RT, bool CODES>
 cudaError_t launch_norm_vec(const NormArgs& a, bool vec, cudaStream_t stream) {
-  if (!vec) return launch_norm_of<XT, RT, 1, false>(a, stream);
-  return a.hidden % 8 == 0 ? launch_norm_of<XT, RT, 8, false>(a, stream) : launch_norm_of<XT, RT, 8, true>(a, stream);
+  if (!vec) return launch_norm_of<XT, RT, 1, false, CODES>(a, stream);
+  return a.hidden % 8 == 0 ? launch_norm_of<XT, RT, 8, false, CODES>(a, stream)
+                           : launch_norm_of<XT, RT, 8, true, CODES>(a, stream);
+}
+
+template <typename XT, typename RT>
+cudaError_t launch_norm_codes(const NormArgs& a, bool vec, cudaStream_t stream) {
+  return a.q_kind != kQuantNone ? launch_norm_vec<XT, RT, true>(a, vec, stream)
+                                : launch_norm_vec<XT, RT, false>(a, vec, stream);
 }
 
 template <typename XT>
 cudaError_t launch_norm_res(const NormArgs& a, int res, bool vec, cudaStream_t stream) {
-  if (a.res == nullptr) return launch_norm_vec<XT, NoResidual>(a, vec, stream);
-  return res ? launch_norm_vec<XT, float>(a, vec, stream) : launch_norm_vec<XT, uint16_t>(a, vec, stream);
+  if (a.res == nullptr) return launch_norm_codes<XT, NoResidual>(a, vec, stream);
+  return res ? launch_norm_codes<XT, float>(a, vec, stream) : launch_norm_codes<XT, uint16_t>(a, vec, stream);
 }
 
 bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
