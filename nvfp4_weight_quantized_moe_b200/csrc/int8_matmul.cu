@@ -9,8 +9,8 @@
 // Small batches take the register-fed kernel of this file, larger ones the
 // tensor-core kernels of int8_matmul_tc.cu (launch_int8_matmul has the rule).
 //
-// Register-fed kernel: one CTA per 16 channels and 8 TT tokens; its warps split
-// K in chunks of 64 and add their sums in shared memory.  mma.m16n8k32 (s8)
+// Register-fed kernel: one CTA per 16 channels and 8 TT tokens; its 4 or 8 warps
+// split K in chunks of 64 and add their sums in shared memory.  mma.m16n8k32 (s8)
 // takes the channels as rows and the tokens as columns.  A lane loads 16
 // consecutive bytes of a row where the instruction wants four runs of four: the
 // k order inside a chunk is permuted, identically for both operands, which a sum
@@ -25,7 +25,6 @@ namespace nvm {
 
 namespace {
 
-constexpr int kRegWarps = 4;
 constexpr int kRegRows = 16;
 
 NVM_DEV void mma_s8_16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -50,9 +49,10 @@ NVM_DEV void store_out(void* out, bool f32, uint64_t at, float v) {
 
 }  // namespace
 
-template <int TT>
-__global__ void __launch_bounds__(32 * kRegWarps) int8_matmul_reg_kernel(const Int8MatmulArgs a) {
-  __shared__ int part[kRegWarps][8 * TT][kRegRows + 1];
+// WARPS split K; each has AHEAD chunks in flight, twice.
+template <int TT, int WARPS, int AHEAD>
+__global__ void __launch_bounds__(32 * WARPS) int8_matmul_reg_kernel(const Int8MatmulArgs a) {
+  __shared__ int part[WARPS][8 * TT][kRegRows + 1];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -65,20 +65,43 @@ __global__ void __launch_bounds__(32 * kRegWarps) int8_matmul_reg_kernel(const I
   const uint4 zero = make_uint4(0, 0, 0, 0);
   int d[TT][4] = {};
   const int K = (int)a.K;
-#pragma unroll 2
-  for (int k0 = 64 * warp; k0 < K; k0 += 64 * kRegWarps) {
-    const bool in = k0 + 16 * c < K;
-    const uint4 u = in && r0 ? ld_stream_v4(w0 + k0) : zero;
-    const uint4 v = in && r1 ? ld_stream_v4(w1 + k0) : zero;
+  // The next AHEAD chunks are on their way while these are multiplied: a weight
+  // byte takes about a microsecond to arrive.
+  struct Chunk {
+    uint4 u, v, b[TT];
+  };
+  Chunk now[AHEAD], next[AHEAD];
+  auto load = [&](Chunk (&chunk)[AHEAD], int k0) {
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const uint32_t m = m0 + 8 * t + g;
-      uint4 b = zero;
-      if (in && m < a.M)
-        b = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.x) + (uint64_t)m * a.ldx + k0 + 16 * c));
-      mma_s8_16832(d[t], u.x, v.x, u.y, v.y, b.x, b.y);
-      mma_s8_16832(d[t], u.z, v.z, u.w, v.w, b.z, b.w);
+    for (int i = 0; i < AHEAD; ++i) {
+      const int k = k0 + 64 * WARPS * i;
+      const bool in = k + 16 * c < K;
+      chunk[i].u = in && r0 ? ld_stream_v4(w0 + k) : zero;
+      chunk[i].v = in && r1 ? ld_stream_v4(w1 + k) : zero;
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const uint32_t m = m0 + 8 * t + g;
+        chunk[i].b[t] = zero;
+        if (in && m < a.M)
+          chunk[i].b[t] =
+              __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.x) + (uint64_t)m * a.ldx + k + 16 * c));
+      }
     }
+  };
+  constexpr int kStep = 64 * WARPS * AHEAD;
+  load(now, 64 * warp);
+  for (int k0 = 64 * warp; k0 < K; k0 += kStep) {
+    if (k0 + kStep < K) load(next, k0 + kStep);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        mma_s8_16832(d[t], now[i].u.x, now[i].v.x, now[i].u.y, now[i].v.y, now[i].b[t].x, now[i].b[t].y);
+        mma_s8_16832(d[t], now[i].u.z, now[i].v.z, now[i].u.w, now[i].v.w, now[i].b[t].z, now[i].b[t].w);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) now[i] = next[i];
   }
   // d[t] holds channels g and g + 8 of tokens 8 t + 2 c, + 1.
 #pragma unroll
@@ -86,12 +109,12 @@ __global__ void __launch_bounds__(32 * kRegWarps) int8_matmul_reg_kernel(const I
 #pragma unroll
     for (int i = 0; i < 4; ++i) part[warp][8 * t + 2 * c + (i & 1)][g + 8 * (i >> 1)] = d[t][i];
   __syncthreads();
-  for (int i = threadIdx.x; i < 8 * TT * kRegRows; i += 32 * kRegWarps) {
+  for (int i = threadIdx.x; i < 8 * TT * kRegRows; i += 32 * WARPS) {
     const uint32_t m = m0 + i / kRegRows, n = n0 + i % kRegRows;
     if (m >= a.M || n >= a.N) continue;
     int sum = 0;
 #pragma unroll
-    for (int w = 0; w < kRegWarps; ++w) sum += part[w][i / kRegRows][i % kRegRows];
+    for (int w = 0; w < WARPS; ++w) sum += part[w][i / kRegRows][i % kRegRows];
     float v = scaled(sum, a.x_scale[m], a.w_scale[n]);
     if (a.bias != nullptr) v += a.bias[n];
     store_out(a.out, a.out_f32, (uint64_t)m * a.ldo + n, v);
@@ -100,11 +123,22 @@ __global__ void __launch_bounds__(32 * kRegWarps) int8_matmul_reg_kernel(const I
 
 namespace {
 
+template <int TT, int WARPS, int AHEAD>
+cudaError_t launch_reg_of(const Int8MatmulArgs& a, uint64_t blocks, cudaStream_t stream) {
+  return launch_pdl(int8_matmul_reg_kernel<TT, WARPS, AHEAD>, dim3((unsigned)blocks), dim3(32 * WARPS), 0, stream, a);
+}
+
 template <int TT>
 cudaError_t launch_reg(const Int8MatmulArgs& a, cudaStream_t stream) {
   const uint64_t blocks = (uint64_t)((a.N + kRegRows - 1) / kRegRows) * ((a.M + 8 * TT - 1) / (8 * TT));
   if (blocks > 0x7fffffffull) return cudaErrorInvalidConfiguration;
-  return launch_pdl(int8_matmul_reg_kernel<TT>, dim3((unsigned)blocks), dim3(32 * kRegWarps), 0, stream, a);
+  // A long K is a chain of round trips to memory: eight warps with as many chunks in
+  // flight as registers allow (1 token, n = k = 4096: 3.6 us, with four warps and one
+  // chunk 7.1).  A short one, or more CTAs than keep every SM busy, is better off
+  // with small CTAs (246 x 336 x 192: 2.1 us against 4.0).
+  constexpr int kLong = TT == 1 ? 4 : 2;
+  if (a.K >= 1024 && blocks <= 4ull * sm_count()) return launch_reg_of<TT, 8, kLong>(a, blocks, stream);
+  return launch_reg_of<TT, 4, 1>(a, blocks, stream);
 }
 
 }  // namespace
@@ -114,36 +148,37 @@ namespace {
 // Which kernel takes a product: the shortest of the estimated times below, in
 // microseconds.  Their forms follow the kernels (rounds of CTAs, a pace per
 // stage of K, bytes through the L2 at a rate, an epilogue); the numbers are a
-// fit to 178 shapes of 1 to 8192 tokens, n 64 to 16384, k 128 to 8192, measured on
-// B200 in all nine forms.  Over those shapes the choice is 1.3 % slower than the
-// best form in the geometric mean, where any single kernel is over 40 %.
+// fit to 286 shapes of 1 to 8192 tokens, n 64 to 8192, k 128 to 8192, measured on
+// B200 in all nine forms.  Over those shapes the choice is 1.0 % slower than the
+// best form in the geometric mean; each of the nine is the best for some.
 struct Form {
   int bn;       // 0: register-fed; 64, 128: tiles of so many channels; 256: CTA pairs
   uint32_t by;  // register-fed: 8-token tiles; tiles: CTAs that split K
 };
 
-double estimate(const Int8MatmulArgs& a, Form f, double sms) {
+double estimate(const Int8MatmulArgs& a, Form f, int sms) {
   auto over = [](uint64_t x, uint64_t y) { return (double)((x + y - 1) / y); };
   const double stages = over(a.K, 128);
   if (f.bn == 0) {
-    const double ctas = over(a.N, 16) * over(a.M, 8 * f.by);
-    const bool one = f.by == 1;
-    return 1.1 + over(a.K, 256) * (one ? 0.29 : 0.44) + ctas * a.K * (16.0 + 8 * f.by) / (one ? 11e6 : 13e6);
+    const double ctas = over(a.N, 16) * over(a.M, 8 * f.by), bytes = ctas * a.K * (16.0 + 8 * f.by);
+    if (f.by == 1) return 1.7 + bytes / 7.1e6;
+    return 1.7 + (a.K >= 1024 && ctas <= 4 * sms ? over(a.K, 1024) * 0.25 : over(a.K, 256) * 0.16) + bytes / 9.0e6;
   }
-  if (f.bn == 256) return 5.1 + std::ceil(over(a.M, 256) * over(a.N, 256) / std::floor(sms / 2)) * stages * 0.39;
-  const double ctas = over(a.M, 128) * over(a.N, f.bn) * f.by, per_sm = std::ceil(ctas / sms);
+  if (f.bn == 256)
+    return 4.5 + std::ceil(over(a.M, 256) * over(a.N, 256) / (sms / 2)) * std::fmax(stages * 0.59, 1.2);
+  const double ctas = over(a.M, 128) * over(a.N, f.bn) * f.by, per_sm = std::ceil(ctas / int8_tile_slots(f.by, sms));
   const double own = std::ceil(stages / f.by), rows = a.M < 128 ? over(a.M, 8) * 8 : 128;
-  const double pace = own * 0.43 * (per_sm == 1 ? 1 : per_sm * 0.59);  // two CTAs of an SM overlap
-  const double bytes = ctas * own * (rows + f.bn) * 128 / 7.8e6;
-  const double tail = f.by == 1 ? per_sm * (f.bn == 64 ? 0.63 : 2.8) : 2.4 + per_sm * 0.57 * (f.bn / 64);
-  return 1.1 + (pace > bytes ? pace : bytes) + tail;
+  const double pace = own * 0.34 * (per_sm == 1 ? 1 : per_sm * 0.65);  // two CTAs of an SM overlap
+  const double bytes = ctas * own * (rows + f.bn) * 128;
+  const double tail = f.by == 1 ? per_sm * (f.bn == 64 ? 0.67 : 3.4) : 1.8 + per_sm * 0.79 * (f.bn / 64);
+  return 2.1 + std::fmax(pace, bytes / 9.7e6) + tail;
 }
 
 }  // namespace
 
 cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, cudaStream_t stream) {
   static constexpr Form kForms[] = {{0, 1}, {0, 2}, {64, 1}, {64, 2}, {64, 4}, {64, 8}, {128, 1}, {128, 4}, {256, 1}};
-  const double sms = sm_count();
+  const int sms = sm_count();
   Form best = kForms[0];
   double least = estimate(a, best, sms);
   for (const Form& f : kForms) {

@@ -604,7 +604,7 @@ cudaError_t launch_int8_pair(const Int8MatmulArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_int8_tile(const Int8MatmulArgs& a, int bn, uint32_t split, cudaStream_t stream) {
   const uint64_t ctas = (uint64_t)((a.M + kTileM - 1) / kTileM) * ((a.N + bn - 1) / bn) * split;
-  const bool deep = ctas <= (uint64_t)sm_count();
+  const bool deep = ctas <= (uint64_t)int8_tile_slots(split, sm_count());
   if (bn == 64) return deep ? launch_tile<64, true>(a, split, stream) : launch_tile<64, false>(a, split, stream);
   return deep ? launch_tile<128, true>(a, split, stream) : launch_tile<128, false>(a, split, stream);
 }

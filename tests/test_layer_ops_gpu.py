@@ -433,16 +433,20 @@ def test_matmul_larger_sizes(nvm, m, n, k):
     _check_matmul(nvm, _codes(g, m, k), _codes(g, n, k), F32, bias=torch.randn(n, generator=g, device="cuda"), seed=k)
 
 
-# Shapes that take each of the tensor-core forms (tiles of 64 and 128 channels, K
-# whole or split over 2, 4, 8 CTAs, CTA pairs), each with n a multiple of 8, even and
-# odd, batches below and above a tile's 128 rows, and k that ends inside a stage.
-FORMS = [(216, 3660, 80), (1428, 465, 96), (775, 880, 96), (64, 4711, 512), (110, 3356, 576), (79, 3696, 896),
-         (772, 1457, 544), (2331, 139, 1664), (2365, 140, 1680), (2767, 136, 1488), (3263, 1, 2512),
-         (3894, 2, 2912), (3767, 8, 2704), (49, 1870, 1472), (92, 1479, 1296), (86, 2208, 1232), (1, 1, 4480),
-         (1, 2, 4704), (2, 96, 3872), (243, 1, 4384), (203, 2, 4016), (138, 8, 4480), (26, 288, 5264),
-         (4442, 326, 784), (404, 3456, 816), (274, 4397, 992), (5, 3686, 4640), (6, 3791, 4672), (10, 3264, 3488),
-         (2866, 66, 1376), (159, 1481, 1184), (3548, 80, 1392), (2091, 2259, 96), (1794, 2708, 96), (4257, 840, 160),
-         (1025, 2305, 2064), (511, 8191, 2048)]
+# Shapes that take each of the forms (register-fed with 8 and 16 tokens and short and
+# long k; tiles of 64 and 128 channels, k whole or split over 2, 4, 8 CTAs; CTA
+# pairs), with n a multiple of 8, even and odd, batches below and above a tile's 128
+# rows, and k that ends inside a stage.
+FORMS = [(1, 1, 4480), (243, 1, 4384), (138, 8, 4480), (26, 288, 5264), (5, 3686, 4640), (6, 9791, 1072),
+         (1330, 1, 1920), (4027, 2, 672), (110, 2426, 48), (49, 1870, 1472), (92, 1479, 1296), (1428, 465, 96),
+         (231, 3924, 96), (226, 3489, 112), (230, 3640, 112), (64, 4711, 512), (110, 3356, 576), (79, 3696, 896),
+         (772, 1457, 544), (4442, 326, 784),
+         (4239, 40, 1584), (33, 4206, 1952), (4194, 46, 1520), (4204, 51, 1472), (45, 4432, 1792), (2331, 139, 1664),
+         (3580, 17, 2848), (3817, 50, 944), (84, 1589, 1440), (166, 944, 1360), (127, 1254, 1472), (126, 1256, 1712),
+         (1717, 19, 4480), (1198, 34, 4464), (65, 774, 4000), (113, 639, 2880), (625, 184, 1888), (89, 960, 3936),
+         (268, 4456, 1520), (140, 4991, 2608), (653, 2830, 1200),
+         (17, 3874, 3216), (2866, 66, 1376), (1470, 131, 1408), (49, 3960, 1408), (72, 2651, 1472), (2260, 72, 2176),
+         (1431, 2413, 80), (2396, 1526, 80), (1832, 2008, 80), (1025, 2305, 2064), (511, 8191, 2048), (2091, 2259, 96)]
 
 
 @pytest.mark.parametrize("m,n,k", FORMS)
