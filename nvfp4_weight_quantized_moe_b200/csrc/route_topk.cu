@@ -117,10 +117,9 @@ struct RouteArgs {
 // What a warp's selection leaves in shared memory.
 struct alignas(16) Picks {
   int id[32];           // the chosen experts, best first; -1 where none is left
-  float logit[32];      // their logits
-  uint32_t key[32];     // candidates in the order of their index: keys (0 past them), ...
-  int expert[32];       // ... experts and
-  float found[32];      // logits
+  float logit[32];      // their logits, where the choice is by logits
+  uint32_t key[32];     // candidates in the order of their index: keys (0 past them)
+  int expert[32];       // ... and experts
   uint2 ranked[32];     // the best of them, best first (key, expert)
 };
 
@@ -290,7 +289,6 @@ __device__ __noinline__ void pick_exactly(const RouteArgs& a, const T* row, Scor
     if (top <= KeyOf<double>::none) break;
     if (lane == __ffs(__ballot_sync(kFull, best == top)) - 1) {
       picks.id[r] = e0 + at;
-      picks.logit[r] = clean_logit(logit_f32<T>(row[e0 + at]));
       key[at] = 0;
     }
   }
@@ -309,10 +307,7 @@ __device__ __noinline__ void rank_exactly(const RouteArgs& a, const T* row, Scor
     const uint64_t k = __shfl_sync(kFull, key, i);
     rank += k > key || (k == key && i < lane);
   }
-  if (lane < n && rank < a.topk) {
-    picks.id[rank] = e;
-    picks.logit[rank] = picks.found[lane];
-  }
+  if (lane < n && rank < a.topk) picks.id[rank] = e;
   __syncwarp();
 }
 
@@ -377,14 +372,23 @@ NVM_DEV void select_experts(const RouteArgs& a, const T* row, const float (&l)[E
         return order_key(a.softmax ? softmax_score(l[j]) : sigmoid_score(l[j]));
       });
     }
-    mask = best_groups(a, mine, kNone);
+    // The best groups one after another; then the worst kept stands against the
+    // best left out (there may be none).
+    mask = 0;
+    uint32_t worst = 0;
+#pragma unroll 1
+    for (int r = 0; r < a.topk_groups; ++r) {
+      const uint32_t top = __reduce_max_sync(kFull, mine);
+      if (top <= kNone) break;
+      const int at = __ffs(__ballot_sync(kFull, mine == top)) - 1;
+      mask |= 1u << at;
+      if (lane == at) mine = 0;
+      worst = top;
+    }
     if (scored || sums) {
-      // The worst kept against the best left out (there may be none).
-      const bool kept = ((mask >> lane) & 1u) != 0;
-      const uint32_t above = __reduce_min_sync(kFull, kept ? mine : 0xffffffffu);
-      const uint32_t below = __reduce_max_sync(kFull, kept ? 0u : mine);
+      const uint32_t below = __reduce_max_sync(kFull, mine);
       if (below > kNone) {
-        const float v = key_value(above, 0.0f);
+        const float v = key_value(worst, 0.0f);
         if (v - key_value(below, 0.0f) <= a.group_top * bound(v))
           mask = groups_exactly<T, EPL>(a, row, scores_exactly<T>(a, row, lmax));
       }
@@ -410,64 +414,64 @@ NVM_DEV void select_experts(const RouteArgs& a, const T* row, const float (&l)[E
 #pragma unroll
   for (int j = 1; j < EPL; ++j) best = key[j] > best ? key[j] : best;
   uint32_t floor = 0, rest = best;
-#pragma unroll 1
+#pragma unroll 4
   for (int s = 0; s < a.topk; ++s) {
     floor = __reduce_max_sync(kFull, rest);
     if (rest == floor) rest = 0;
   }
+  auto lower = [&](uint32_t from) {
+    if (scored) {
+      const float v = key_value(from, 0.0f), under = v - bound(v);
+      if (under < v) from = order_key(under);  // not of an infinity
+    }
+    return from > kNone ? from : kNone + 1;
+  };
   auto candidates = [&](uint32_t from) {  // of this lane
     int c = 0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) c += key[j] >= from;
     return c;
   };
-  if (floor <= kNone) floor = kNone + 1;
-  int n = __reduce_add_sync(kFull, candidates(floor));
-  if (n > 32) {
+  uint32_t bar = lower(floor);
+  int count = candidates(bar);
+  if (__reduce_add_sync(kFull, count) > 32) {
     // Bisect for a higher bar that topk to 32 experts pass (there is none where
     // too many are equal).
     uint32_t over = __reduce_max_sync(kFull, best) + 1;
+    int n = 33;
 #pragma unroll 1
     while (over - floor > 1 && n > 32) {
       const uint32_t middle = floor + (over - floor) / 2;
-      const int c = __reduce_add_sync(kFull, candidates(middle));
-      if (c < a.topk) {
+      if ((int)__reduce_add_sync(kFull, candidates(middle)) < a.topk) {
         over = middle;
       } else {
         floor = middle;
-        n = c;
+        bar = lower(floor);
+        count = candidates(bar);
+        n = __reduce_add_sync(kFull, count);
       }
     }
   }
-  if (scored) {
-    const float v = key_value(floor, 0.0f);
-    const float under = v - bound(v);
-    if (under < v) floor = order_key(under);  // not of an infinity
-    if (floor <= kNone) floor = kNone + 1;
-  }
-  const int count = candidates(floor);
   int upto = count;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(kFull, upto, o);
     if (lane >= o) upto += v;
   }
-  n = __shfl_sync(kFull, upto, 31);
+  const int n = __shfl_sync(kFull, upto, 31);
   __syncwarp();
   if (n <= 32) {
     if (count > 0) {
       int at = upto - count;
 #pragma unroll
       for (int j = 0; j < EPL; ++j)
-        if (key[j] >= floor) {
+        if (key[j] >= bar) {
           picks.key[at] = key[j];
-          picks.expert[at] = e0 + j;
-          picks.found[at++] = l[j];
+          picks.expert[at++] = e0 + j;
         }
     }
     __syncwarp();
     const uint2 c = make_uint2(picks.key[lane], (uint32_t)picks.expert[lane]);
-    const float logit = picks.found[lane];
     int rank = 0;
 #pragma unroll 1
     for (int i = 0; i < n; i += 4) {
@@ -480,7 +484,7 @@ NVM_DEV void select_experts(const RouteArgs& a, const T* row, const float (&l)[E
     }
     if (lane < n && rank < a.topk) {
       picks.id[rank] = (int)c.y;
-      picks.logit[rank] = logit;
+      picks.logit[rank] = key_value(c.x, 0.0f);  // where the choice is by logits
     }
     if (scored) {
       if (lane < n) picks.ranked[rank] = c;
@@ -563,7 +567,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, EPL <= 8 ? 8 : EPL == 16 ? 6 :
   // logit, so they are never 0 / 0: softmax exp(l - top); sigmoid
   // exp(l - base) / (1 + exp(l)) with base = min(0, top).
   const int id = picks.id[lane];
-  const float x = id >= 0 ? picks.logit[lane] : -INFINITY;
+  float x = -INFINITY;
+  if (id >= 0) x = a.bias == nullptr ? picks.logit[lane] : clean_logit(logit_f32<T>(__ldg(row + id)));
   float base = a.softmax ? lmax : 0.0f;
   if (a.renorm) {
     base = key_value(__reduce_max_sync(kFull, order_key(x)), 0.0f);
@@ -571,9 +576,14 @@ __global__ void __launch_bounds__(32 * kMaxWarps, EPL <= 8 ? 8 : EPL == 16 ? 6 :
   }
   float w = 0.0f;
   if (id >= 0) {
-    const float low = expf(fminf(x, a.softmax ? x : 0.0f) - base);
-    w = low;
-    if (!a.softmax) w = x > 0.0f ? __fdividef(1.0f, 1.0f + expf(-x)) : __fdividef(low, 1.0f + expf(x));
+    if (a.softmax) {
+      w = expf(x - base);
+    } else if (base < 0.0f) {
+      w = __fdividef(expf(x - base), 1.0f + expf(x));
+    } else {
+      const float t = expf(-fabsf(x));
+      w = __fdividef(x > 0.0f ? 1.0f : t, 1.0f + t);
+    }
   }
   float norm = a.softmax ? zinv : 1.0f;
   if (a.renorm) {
