@@ -20,6 +20,14 @@
 // first CTA issues, warps 2-9 drain (two per TMEM lane quarter, half of the
 // columns each).
 //
+// Measured: 8192 x 8192 x 4096 (tokens, n, k) 173 to 179 us, 3.1 to 3.2 * 10^15
+// operations a second, 94 to 97 % of twice the measured BF16 rate; 4096 x 8192 x 4096 with
+// the tensor pipe 76 % busy from launch to end.  What is left there is the first
+// tiles' arrival and the last ones' epilogue (about 3 us each), and, below k of about
+// 1000, the outputs: 3 us per round of tiles.  Tiles: 256 x 2048 x 7168 in 128 CTAs
+// 10.2 us, bound by the operands' way from the L2 (88 KB a microsecond and SM) and
+// 5 us of launch, cluster exchange and epilogue.
+//
 // Every wait is bounded; on timeout a CTA flags the device error word and skips
 // its remaining waits.
 

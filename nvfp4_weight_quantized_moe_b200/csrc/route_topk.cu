@@ -18,9 +18,13 @@
 // ballot, and where a group is whole lanes the best two of all groups are found
 // at once by a butterfly inside the group's lanes.  Maxima are single redux
 // instructions on order-preserving integer keys.  Lane s ends up with choice s,
-// so topk <= 32 and num_groups <= 32.  The work is one read of the logits; per
-// token it is a chain of topk dependent warp reductions, hidden by the other
-// warps of the SM for large batches.
+// so topk <= 32 and num_groups <= 32.
+//
+// The work is one read of the logits (8191 x 256 FP32: 1.4 us at the copy
+// bandwidth); what bounds it is instruction issue, about 890 warp instructions a
+// token with scores, bias and groups (8191 x 256: 13 us, 68 % of the issue slots),
+// 600 without (8192 x 128 BF16: 7.7 us), and for one token the chain of warp
+// reductions (2.0 us and 3.5 us with groups, of which 1.3 us are the launch).
 
 #include <cfloat>
 #include <climits>

@@ -244,6 +244,30 @@ def test_route_feeds_the_sort_and_the_forward(nvm):
         assert orc.relative_l2(bufs.out.cpu().numpy().astype(np.float64), ref["out"]) <= 1e-3
 
 
+@pytest.mark.parametrize("kind", ["shared", "nongated", "steps"])
+def test_forward_logits_is_routing_then_forward(nvm, kind):
+    from workloads import make_problem
+    from workloads.device import upload_inputs, upload_layer
+    from workloads.generators import MoEConfig
+
+    prob = make_problem(MoEConfig("routed", 256, 512, 8, 2, 21, "uniform", 88))
+    layer = upload_layer(prob, shared=kind == "shared", activation="relu2" if kind == "nongated" else None)
+    x, _, _ = upload_inputs(prob)
+    router = nvm.MoERouter(2, score="sigmoid", bias=torch.linspace(-0.1, 0.1, 8, device="cuda"), scale=2.0)
+    logits = torch.randn(21, 8, generator=_gen(2), device="cuda").to(BF16)
+    ids, w = torch.empty(21, 2, dtype=torch.int32, device="cuda"), torch.empty(21, 2, device="cuda")
+    router.route(logits, ids, w)
+    opts = dict(steps=True) if kind == "steps" else {}
+    want = layer.forward(x, ids, w, workspace=layer.workspace(21), **opts)
+    got = layer.forward_logits(x, logits, router, layer.buffers(30), workspace=layer.workspace(21), **opts)
+    torch.cuda.synchronize()
+    assert torch.equal(got.routed_ids[:21], ids) and torch.equal(got.routed_weights[:21], w)
+    assert torch.equal(got.out[:21], want.out[:21]) and float(want.out.abs().max()) > 0
+    for bad in (dict(logits=logits[:20]), dict(router=nvm.MoERouter(3))):
+        with pytest.raises(ValueError):
+            layer.forward_logits(x, bad.get("logits", logits), bad.get("router", router))
+
+
 # --------------------------------------------------------------------------- #
 # Norm
 # --------------------------------------------------------------------------- #
@@ -662,6 +686,11 @@ def test_the_binding_refuses_wrong_tensors(nvm):
         nvm.route_topk(l, ids, w, bias=torch.zeros(15, **cuda))
     with pytest.raises(nvm.NVFP4MoEError):
         nvm.route_topk(l, ids, w, num_groups=3)
+    for bad in (dict(num_groups=-1), dict(topk_groups=1 << 40), dict(scale=1e300)):
+        with pytest.raises((ValueError, nvm.NVFP4MoEError)):
+            nvm.route_topk(l, ids, w, **bad)
+    with pytest.raises(AttributeError):
+        nvm.route_topk(None, ids, w)
 
     x, g, out = torch.zeros(4, 16, **cuda), torch.ones(16, **cuda), torch.zeros(4, 16, dtype=BF16, **cuda)
     q, s = torch.zeros(4, 16, dtype=INT8, **cuda), torch.zeros(4, **cuda)
