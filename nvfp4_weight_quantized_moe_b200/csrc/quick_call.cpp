@@ -83,6 +83,12 @@ uint32_t u32(PyObject* o) {
   return u32((int64_t)v);
 }
 
+int32_t truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Unusual{};
+  return v;
+}
+
 float f32(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (PyErr_Occurred()) throw Unusual{};
@@ -134,7 +140,7 @@ PyObject* route_topk(PyObject*, PyObject* const* v, Py_ssize_t n) {
     a.num_groups = u32(v[5]);
     a.topk_groups = u32(v[6]);
     a.group_top = u32(v[7]);
-    a.renormalize = PyObject_IsTrue(v[8]) == 1;
+    a.renormalize = truth(v[8]);
     a.scale = f32(v[9]);
     return launch(g_route, a, dev);
   });

@@ -608,7 +608,7 @@ namespace {
 template <typename T>
 cudaError_t launch_route_topk_of(const RouteArgs& a, cudaStream_t stream) {
   // One warp per CTA while that leaves every SM at most a few tokens (their
-  // chains then run on separate schedulers), eight for large batches.
+  // chains then run on separate schedulers), four for large batches.
   const int warps = a.M <= 592 ? 1 : kMaxWarps;
   const dim3 grid((a.M + warps - 1) / warps), block(32 * warps);
   const int epl = a.per_lane;

@@ -722,6 +722,16 @@ def test_the_binding_refuses_wrong_tensors(nvm):
         nvm.int8_matmul(q[:, :8], s, wq[:, :8].contiguous(), ws, o)
 
 
+def test_arguments_that_have_no_truth_value(nvm):
+    cuda = dict(device="cuda")
+    l, ids, w = torch.zeros(4, 16, **cuda), torch.zeros(4, 2, dtype=torch.int32, **cuda), torch.zeros(4, 2, **cuda)
+    with pytest.raises(RuntimeError):  # of a tensor of two values, as everywhere in Python
+        nvm.route_topk(l, ids, w, renormalize=torch.ones(2))
+    nvm.route_topk(l, ids, w, renormalize=torch.ones(1))
+    torch.cuda.synchronize()
+    assert torch.equal(w, torch.full_like(w, 0.5))
+
+
 def test_empty_batches(nvm):
     cuda = dict(device="cuda")
     nvm.route_topk(torch.empty(0, 16, **cuda), torch.empty(0, 2, dtype=torch.int32, **cuda), torch.empty(0, 2, **cuda))
