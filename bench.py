@@ -63,11 +63,11 @@ KERNEL_SOURCES = {
 # kernel, with the hash of that kernel's sources when it was captured.  An
 # entry whose hash no longer matches the sources is stale and not reported.
 NCU_TRAFFIC_BYTES = {
-    ("decode_m1", "mma.sync"): (28362496, "75ef290dff45"),       # 28.36 MB read, 0.002 MB written
-    ("decode_m32", "tcgen05"): (297321728, "f284aa1030ca"),      # 293.13 MB read, 4.19 MB written
+    ("decode_m1", "mma.sync"): (28360704, "bb9c7e7e475e"),       # 28.36 MB read, nothing written
+    ("decode_m32", "tcgen05"): (297628160, "ae177aecb779"),      # 293.12 MB read, 4.51 MB written
     # reduced case (64 experts, 64 tokens: the same 8 rows per expert) x 4 experts
-    ("decode_m256", "tcgen05"): (4515166208, "f284aa1030ca"),    # 4 x (1122.08 + 6.71) MB
-    ("prefill_m8192", "tcgen05"): (3189124864, "f284aa1030ca"),  # 2.7995 GB read, 0.3896 GB written
+    ("decode_m256", "tcgen05"): (4517625856, "ae177aecb779"),    # 4 x (1122.61 + 6.80) MB
+    ("prefill_m8192", "tcgen05"): (3110805760, "ae177aecb779"),  # 2.7205 GB read, 0.3903 GB written
 }
 # Entries not captured on the workload itself: how the figure was obtained.
 NCU_TRAFFIC_SCALED = {
