@@ -20,19 +20,18 @@
 // first CTA issues, warps 2-9 drain (two per TMEM lane quarter, half of the
 // columns each).
 //
-// Measured: 8192 x 8192 x 4096 (tokens, n, k) 173 to 179 us, 3.1 to 3.2 * 10^15
-// operations a second, 94 to 97 % of twice the measured BF16 rate; 4096 x 8192 x 4096 with
-// the tensor pipe 76 % busy from launch to end.  What is left there is the first
-// tiles' arrival and the last ones' epilogue (about 3 us each), and, below k of about
-// 1000, the outputs: 3 us per round of tiles.  Tiles: 256 x 2048 x 7168 in 128 CTAs
-// 10.2 us, bound by the operands' way from the L2 (88 KB a microsecond and SM) and
-// 5 us of launch, cluster exchange and epilogue.
+// Measured: 8192 x 8192 x 4096 (tokens, n, k) 169 us, 3.25 * 10^15 operations a second,
+// 99 % of twice the measured BF16 rate.  Below k of about 1000 the outputs bound it: 3 us
+// per round of tiles.  Tiles: 256 x 2048 x 7168 in 128 CTAs 9.0 us, of which 5 are launch,
+// cluster exchange and epilogue, the rest the operands' way from the L2.
 //
 // Every wait is bounded; on timeout a CTA flags the device error word and skips
 // its remaining waits.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -163,17 +162,27 @@ NVM_DEV int4 ld_cluster_int4(uint32_t addr) {
                : "memory");
   return v;
 }
+// One lane of the warp, in a form from which the compiler sees that it is one.  The
+// operands of copies and products live in the warp's uniform registers: with a whole
+// warp that loops and one elected lane that issues they stay there, while behind
+// `lane == 0` a product took 112 cycles to issue whatever its size (128 x 2048 x 8192 in
+// 32 tiles: 18.1 us, elected 11.3; 8192 x 8192 x 4096 in pairs: 176 and 169).
+NVM_DEV bool elect_one() {
+  uint32_t v;
+  asm volatile("{.reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p;}" : "=r"(v));
+  return v != 0;
+}
 NVM_DEV void tmap_prefetch(const void* tmap) { asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory"); }
 
-// DEEP: a ring that takes the SM, for grids of at most one CTA per SM, with two
-// stages of K to a barrier: what bounds one CTA there is the issuing thread's way
-// from barrier to barrier, about 0.28 us, not its products (128 x 4096 x 4096 in 64
-// CTAs: 12.1 us with one stage to a barrier, 9.8 with two).  Two CTAs of an SM hide
-// each other's.
+// DEEP: a ring that takes the SM, for grids of at most one CTA per SM.  With 64
+// channels a barrier is for two stages of K: the four products of a stage take 0.07 us,
+// less than the way from barrier to barrier (128 x 2048 x 8192 without a split: 12.8 us
+// with one stage to a barrier, 11.3 with two; 128 channels 14.5 and 15.3).  Two CTAs of
+// an SM hide each other's.
 template <int BN, bool DEEP>
 struct TileCfg {
-  static constexpr int GROUP = DEEP ? 2 : 1;          // stages to a barrier
-  static constexpr int STAGES = BN == 128 ? 3 : 4;    // groups in the ring
+  static constexpr int GROUP = DEEP && BN == 64 ? 2 : 1;      // stages to a barrier
+  static constexpr int STAGES = BN == 64 ? 4 : DEEP ? 6 : 3;  // groups in the ring
   static constexpr int A_BYTES = kTileM * kStageK;
   static constexpr int B_BYTES = BN * kStageK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
@@ -212,7 +221,7 @@ __global__ void __launch_bounds__(kTileThreads)
   float* scales = reinterpret_cast<float*>(smem + C::OFF_SCALE);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEM);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (tid == 0) {
     tmap_prefetch(&tm_x);
@@ -253,12 +262,13 @@ __global__ void __launch_bounds__(kTileThreads)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t i = 0;
-      for (uint32_t st = st_lo; st < st_hi; st += C::GROUP, ++i) {
-        const uint32_t slot = i % C::STAGES, round = i / C::STAGES;
-        if (round > 0 && !wait(empty + 8 * slot, (round - 1) & 1)) break;
-        const uint32_t bar = full + 8 * slot, n = min((uint32_t)C::GROUP, st_hi - st);
+    const bool one = elect_one();
+    uint32_t i = 0;
+    for (uint32_t st = st_lo; st < st_hi; st += C::GROUP, ++i) {
+      const uint32_t slot = i % C::STAGES, round = i / C::STAGES;
+      if (round > 0 && !__all_sync(0xffffffffu, wait(empty + 8 * slot, (round - 1) & 1))) break;
+      const uint32_t bar = full + 8 * slot, n = min((uint32_t)C::GROUP, st_hi - st);
+      if (one) {
         mbar_arrive_expect_tx(bar, n * (x_rows * kStageK + C::B_BYTES));
         for (uint32_t g = 0; g < n; ++g) {
           const uint32_t dst = s_base + slot * C::GROUP_BYTES + g * C::STAGE_BYTES;
@@ -266,19 +276,21 @@ __global__ void __launch_bounds__(kTileThreads)
           tma_load_2d(dst + C::A_BYTES, &tm_w, (int)((st + g) * kStageK), (int)n0, bar);
         }
       }
-      // Nothing may still land in this CTA's memory when it goes on.
-      for (uint32_t j = i > (uint32_t)C::STAGES ? i - C::STAGES : 0; j < i; ++j)
-        mbar_wait(full + 8 * (j % C::STAGES), (j / C::STAGES) & 1);
+      __syncwarp();
     }
+    // Nothing may still land in this CTA's memory when it goes on.
+    for (uint32_t j = i > (uint32_t)C::STAGES ? i - C::STAGES : 0; j < i; ++j)
+      mbar_wait(full + 8 * (j % C::STAGES), (j / C::STAGES) & 1);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_s8_s32(kTileM, BN);
-      uint32_t i = 0;
-      for (uint32_t st = st_lo; st < st_hi; st += C::GROUP, ++i) {
-        const uint32_t slot = i % C::STAGES;
-        if (!wait(full + 8 * slot, (i / C::STAGES) & 1)) break;
-        tc_fence_after();
+    constexpr uint32_t idesc = idesc_s8_s32(kTileM, BN);
+    const bool one = elect_one();
+    uint32_t i = 0;
+    for (uint32_t st = st_lo; st < st_hi; st += C::GROUP, ++i) {
+      const uint32_t slot = i % C::STAGES;
+      if (!__all_sync(0xffffffffu, wait(full + 8 * slot, (i / C::STAGES) & 1))) break;
+      tc_fence_after();
+      if (one) {
 #pragma unroll
         for (int g = 0; g < C::GROUP; ++g) {
           if (st + g >= st_hi) break;
@@ -290,9 +302,11 @@ __global__ void __launch_bounds__(kTileThreads)
         }
         tc_commit(empty + 8 * slot);
       }
-      tc_commit(done);
-      mbar_wait(done, 0);  // no MMA may still run when the tensor memory is freed
+      __syncwarp();
     }
+    if (one) tc_commit(done);
+    __syncwarp();
+    mbar_wait(done, 0);  // no MMA may still run when the tensor memory is freed
     __syncwarp();
   } else {
     const int q = warp & 3, row = 32 * q + lane;
@@ -342,51 +356,66 @@ __global__ void __launch_bounds__(kTileThreads)
   const int rows = (int)((there + split - 1) / split);
   const int row_lo = (int)rank * rows;
   const bool vec = a.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (a.out_f32 ? 16 : 8) == 0;
+  // All of a thread's reads are on their way at once, and each CTA begins with its own
+  // sums, so that they do not all read the same one's (128 x 4096 x 4096 in pairs: 9.5
+  // to 9.0 us).
+  auto sum_rows = [&](auto ctas) {
+    constexpr uint32_t kSplit = decltype(ctas)::value;
+    uint32_t part[kSplit];
+#pragma unroll
+    for (uint32_t p = 0; p < kSplit; ++p) part[p] = mapa_shared(s_base, (rank + p) % kSplit);
 #pragma unroll 2
-  for (int i = tid; i < rows * (BN / 4); i += kTileThreads) {
-    const int r = row_lo + i / (BN / 4), c = i % (BN / 4) * 4;
-    const uint32_t m = m0 + r, n = n0 + c;
-    if (r >= (int)there || n >= a.N) continue;
-    const uint32_t at = s_base + (uint32_t)(r * C::PITCH + c) * 4;
-    int4 s = make_int4(0, 0, 0, 0);
-    for (uint32_t p = 0; p < split; ++p) {
-      const int4 v = ld_cluster_int4(mapa_shared(at, p));
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
-    const float xs = scales[r];
-    const float4 ws = *reinterpret_cast<const float4*>(scales + kTileM + c);
-    float4 v = make_float4(scaled(s.x, xs, ws.x), scaled(s.y, xs, ws.y), scaled(s.z, xs, ws.z), scaled(s.w, xs, ws.w));
-    if (a.bias != nullptr) {
-      const float4 b = *reinterpret_cast<const float4*>(scales + kTileM + BN + c);
-      v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
-    }
-    const uint64_t o = (uint64_t)m * a.ldo + n;
-    if (a.out_f32) {
-      float* out = static_cast<float*>(a.out) + o;
-      if (vec && n + 4 <= a.N) {
-        *reinterpret_cast<float4*>(out) = v;
-      } else {
-        out[0] = v.x;
-        if (n + 1 < a.N) out[1] = v.y;
-        if (n + 2 < a.N) out[2] = v.z;
-        if (n + 3 < a.N) out[3] = v.w;
+    for (int i = tid; i < rows * (BN / 4); i += kTileThreads) {
+      const int r = row_lo + i / (BN / 4), c = i % (BN / 4) * 4;
+      const uint32_t m = m0 + r, n = n0 + c;
+      if (r >= (int)there || n >= a.N) continue;
+      const uint32_t at = (uint32_t)(r * C::PITCH + c) * 4;
+      int4 sums[kSplit];
+#pragma unroll
+      for (uint32_t p = 0; p < kSplit; ++p) sums[p] = ld_cluster_int4(part[p] + at);
+      int4 s = sums[0];
+#pragma unroll
+      for (uint32_t p = 1; p < kSplit; ++p) {
+        s.x += sums[p].x;
+        s.y += sums[p].y;
+        s.z += sums[p].z;
+        s.w += sums[p].w;
       }
-    } else {
-      uint16_t* out = static_cast<uint16_t*>(a.out) + o;
-      const uint32_t lo = bf16_pair(v.x, v.y), hi = bf16_pair(v.z, v.w);
-      if (vec && n + 4 <= a.N) {
-        *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+      const float xs = scales[r];
+      const float4 ws = *reinterpret_cast<const float4*>(scales + kTileM + c);
+      float4 v = make_float4(scaled(s.x, xs, ws.x), scaled(s.y, xs, ws.y), scaled(s.z, xs, ws.z), scaled(s.w, xs, ws.w));
+      if (a.bias != nullptr) {
+        const float4 b = *reinterpret_cast<const float4*>(scales + kTileM + BN + c);
+        v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+      }
+      const uint64_t o = (uint64_t)m * a.ldo + n;
+      if (a.out_f32) {
+        float* out = static_cast<float*>(a.out) + o;
+        if (vec && n + 4 <= a.N) {
+          *reinterpret_cast<float4*>(out) = v;
+        } else {
+          out[0] = v.x;
+          if (n + 1 < a.N) out[1] = v.y;
+          if (n + 2 < a.N) out[2] = v.z;
+          if (n + 3 < a.N) out[3] = v.w;
+        }
       } else {
-        out[0] = (uint16_t)lo;
-        if (n + 1 < a.N) out[1] = (uint16_t)(lo >> 16);
-        if (n + 2 < a.N) out[2] = (uint16_t)hi;
-        if (n + 3 < a.N) out[3] = (uint16_t)(hi >> 16);
+        uint16_t* out = static_cast<uint16_t*>(a.out) + o;
+        const uint32_t lo = bf16_pair(v.x, v.y), hi = bf16_pair(v.z, v.w);
+        if (vec && n + 4 <= a.N) {
+          *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+        } else {
+          out[0] = (uint16_t)lo;
+          if (n + 1 < a.N) out[1] = (uint16_t)(lo >> 16);
+          if (n + 2 < a.N) out[2] = (uint16_t)hi;
+          if (n + 3 < a.N) out[3] = (uint16_t)(hi >> 16);
+        }
       }
     }
-  }
+  };
+  if (split == 2) sum_rows(std::integral_constant<uint32_t, 2>());
+  else if (split == 4) sum_rows(std::integral_constant<uint32_t, 4>());
+  else sum_rows(std::integral_constant<uint32_t, 8>());
   // A CTA's sums stay until every CTA of its cluster has read them.
   cluster_sync();
 }
@@ -457,7 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t dfree = done + 16;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEM);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
 
   if (tid == 0) {
@@ -500,55 +529,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t lead_full = mapa_shared(full, 0);
-      uint32_t i = 0;
-      for (uint32_t t = pair; t < ntile && !*abort_flag; t += npairs) {
-        const int y_x = (int)(t % tiles_m * kPairM + rank * (kPairM / 2));
-        const int y_w = (int)(t / tiles_m * kPairN + rank * (kPairN / 2));
-        for (uint32_t st = 0; st < nst; ++st, ++i) {
-          const uint32_t slot = i % C::STAGES, round = i / C::STAGES;
-          if (round > 0 && !wait(empty + 8 * slot, (round - 1) & 1)) break;
-          const uint32_t dst = s_base + slot * C::STAGE_BYTES;
+    const bool one = elect_one();
+    const uint32_t lead_full = mapa_shared(full, 0);
+    uint32_t i = 0;
+    bool ok = true;
+    for (uint32_t t = pair; t < ntile && ok; t += npairs) {
+      const int y_x = (int)(t % tiles_m * kPairM + rank * (kPairM / 2));
+      const int y_w = (int)(t / tiles_m * kPairN + rank * (kPairN / 2));
+      for (uint32_t st = 0; st < nst; ++st, ++i) {
+        const uint32_t slot = i % C::STAGES, round = i / C::STAGES;
+        ok = round == 0 || __all_sync(0xffffffffu, wait(empty + 8 * slot, (round - 1) & 1));
+        if (!ok) break;
+        const uint32_t dst = s_base + slot * C::STAGE_BYTES;
+        if (one) {
           // The first CTA's barrier counts both CTAs' bytes.
           if (rank == 0) mbar_arrive_expect_tx(full + 8 * slot, 2 * C::STAGE_BYTES);
           tma_load_2d_pair(dst, &tm_x, (int)(st * kStageK), y_x, lead_full + 8 * slot);
           tma_load_2d_pair(dst + C::A_BYTES, &tm_w, (int)(st * kStageK), y_w, lead_full + 8 * slot);
         }
-      }
-      // The last stages' products read them: wait for those, and in the first CTA
-      // for its full barriers, which count both CTAs' bytes.
-      for (uint32_t j = i > (uint32_t)C::STAGES ? i - C::STAGES : 0; j < i; ++j) {
-        mbar_wait(empty + 8 * (j % C::STAGES), (j / C::STAGES) & 1);
-        if (rank == 0) mbar_wait(full + 8 * (j % C::STAGES), (j / C::STAGES) & 1);
+        __syncwarp();
       }
     }
+    // The last stages' products read them: wait for those, and in the first CTA
+    // for its full barriers, which count both CTAs' bytes.
+    for (uint32_t j = i > (uint32_t)C::STAGES ? i - C::STAGES : 0; j < i; ++j) {
+      mbar_wait(empty + 8 * (j % C::STAGES), (j / C::STAGES) & 1);
+      if (rank == 0) mbar_wait(full + 8 * (j % C::STAGES), (j / C::STAGES) & 1);
+    }
+    __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       constexpr uint32_t idesc = idesc_s8_s32(kPairM, kPairN);
+      const bool one = elect_one();
       uint32_t i = 0, n = 0;
       for (uint32_t t = pair; t < ntile; t += npairs, ++n) {
         const uint32_t db = n & 1;
         if (n >= 2) {
           wait(dfree + 8 * db, (n / 2 - 1) & 1);
+          __syncwarp();
           tc_fence_after();
         }
         const uint32_t dcol = tmem + db * kPairN;
         for (uint32_t st = 0; st < nst; ++st, ++i) {
           const uint32_t slot = i % C::STAGES;
-          if (!wait(full + 8 * slot, (i / C::STAGES) & 1)) break;
+          if (!__all_sync(0xffffffffu, wait(full + 8 * slot, (i / C::STAGES) & 1))) break;
           tc_fence_after();
           const uint32_t abase = s_base + slot * C::STAGE_BYTES, bbase = abase + C::A_BYTES;
+          if (one) {
 #pragma unroll
-          for (int k = 0; k < kStageK / 32; ++k)
-            tc_mma_pair_s8_ss(dcol, smem_desc_sw128(abase + 32 * k), smem_desc_sw128(bbase + 32 * k), idesc,
-                              st > 0 || k > 0 ? 1u : 0u);
-          tc_commit_pair(empty + 8 * slot, 0x3);
+            for (int k = 0; k < kStageK / 32; ++k)
+              tc_mma_pair_s8_ss(dcol, smem_desc_sw128(abase + 32 * k), smem_desc_sw128(bbase + 32 * k), idesc,
+                                st > 0 || k > 0 ? 1u : 0u);
+            tc_commit_pair(empty + 8 * slot, 0x3);
+          }
+          __syncwarp();
         }
-        tc_commit_pair(done + 8 * db, 0x3);
+        if (one) tc_commit_pair(done + 8 * db, 0x3);
+        __syncwarp();
       }
       // No product may still run when the tensor memory is freed.
       if (n > 0) mbar_wait(done + 8 * ((n - 1) & 1), ((n - 1) / 2) & 1);
+      __syncwarp();
     }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
