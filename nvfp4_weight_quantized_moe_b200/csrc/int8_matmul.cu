@@ -168,7 +168,7 @@ double estimate(const Int8MatmulArgs& a, Form f, int sms) {
   }
   if (f.bn == 256)
     return 4.5 + std::ceil(over(a.M, 256) * over(a.N, 256) / (sms / 2)) * std::fmax(stages * 0.59, 1.2);
-  const double ctas = over(a.M, 128) * over(a.N, f.bn) * f.by, per_sm = std::ceil(ctas / int8_tile_slots(f.by, sms));
+  const double ctas = over(a.M, 128) * over(a.N, f.bn) * f.by, per_sm = std::ceil(ctas / int8_tile_slots(f.by));
   const double own = std::ceil(stages / f.by), rows = a.M < 128 ? over(a.M, 8) * 8 : 128;
   const double pace = own * 0.34 * (per_sm == 1 ? 1 : per_sm * 0.65);  // two CTAs of an SM overlap
   const double bytes = ctas * own * (rows + f.bn) * 128;

@@ -31,6 +31,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -651,9 +652,40 @@ cudaError_t launch_int8_pair(const Int8MatmulArgs& a, cudaStream_t stream) {
   return launch_pdl(int8_pair_kernel, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), C::SMEM, stream, a, x, w);
 }
 
+int int8_tile_slots(uint32_t split) {
+  const int sms = sm_count();
+  if (split < 4) return sms;
+  // The answer for a device does not change: asked once.
+  static std::atomic<int> known[64][2];
+  int dev = 0, clusters = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sms * 3 / 4;
+  std::atomic<int>& slots = known[dev][split == 8];
+  if (const int n = slots.load(std::memory_order_relaxed)) return n;
+  using C = TileCfg<64, true>;
+  const void* kern = reinterpret_cast<const void*>(int8_tile_kernel<64, true>);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(split);
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (ensure_dynamic_smem(kern, C::SMEM) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1) {
+    cudaGetLastError();
+    clusters = sms * 3 / 4 / (int)split;
+  }
+  slots.store(clusters * (int)split, std::memory_order_relaxed);
+  return clusters * (int)split;
+}
+
 cudaError_t launch_int8_tile(const Int8MatmulArgs& a, int bn, uint32_t split, cudaStream_t stream) {
   const uint64_t ctas = (uint64_t)((a.M + kTileM - 1) / kTileM) * ((a.N + bn - 1) / bn) * split;
-  const bool deep = ctas <= (uint64_t)int8_tile_slots(split, sm_count());
+  const bool deep = ctas <= (uint64_t)int8_tile_slots(split);
   if (bn == 64) return deep ? launch_tile<64, true>(a, split, stream) : launch_tile<64, false>(a, split, stream);
   return deep ? launch_tile<128, true>(a, split, stream) : launch_tile<128, false>(a, split, stream);
 }

@@ -163,10 +163,10 @@ cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, cudaStream_t stream);
 // Its tensor-core forms (int8_matmul_tc.cu): 128 x bn tiles (bn 64 or 128) with K
 // split over a cluster of `split` CTAs (1, 2, 4, 8); 256 x 256 tiles by CTA pairs.
 cudaError_t launch_int8_tile(const Int8MatmulArgs& a, int bn, uint32_t split, cudaStream_t stream);
-// SMs that clusters of `split` CTAs can fill with one CTA each: a cluster stays in
-// one GPC, whose 16 to 20 SMs are no multiple of 4 or 8 (144 CTAs in fours took
-// two rounds: 342 x 1488 x 2400 13.4 us, in 72 whole tiles 8.2).
-inline int int8_tile_slots(uint32_t split, int sms) { return split >= 4 ? sms * 7 / 8 : sms; }
+// SMs that clusters of `split` CTAs can fill with one CTA each on the current device: a
+// cluster stays in one GPC, whose SMs are no multiple of 4 or 8 (a 16th cluster of eight
+// waited for a second round: 20 x 1008 x 8192 9.0 us, with two CTAs to an SM 5.9).
+int int8_tile_slots(uint32_t split);
 cudaError_t launch_int8_pair(const Int8MatmulArgs& a, cudaStream_t stream);
 
 cudaError_t launch_append_shared(const int32_t* ids, const float* w, const float* shared_w,
