@@ -150,8 +150,8 @@ namespace {
 // Which kernel takes a product: the shortest of the estimated times below, in
 // microseconds.  Their forms follow the kernels (rounds of CTAs, a pace per
 // stage of K, bytes through the L2 at a rate, an epilogue); the numbers are a
-// fit to 286 shapes of 1 to 8192 tokens, n 64 to 8192, k 128 to 8192, measured on
-// B200 in all nine forms.  Over those shapes the choice is 1.0 % slower than the
+// fit to 446 shapes of 1 to 8192 tokens, n 64 to 8192, k 128 to 8192, measured on
+// B200 in all nine forms.  Over those shapes the choice is 1.2 % slower than the
 // best form in the geometric mean; each of the nine is the best for some.
 struct Form {
   int bn;       // 0: register-fed; 64, 128: tiles of so many channels; 256: CTA pairs
@@ -163,17 +163,25 @@ double estimate(const Int8MatmulArgs& a, Form f, int sms) {
   const double stages = over(a.K, 128);
   if (f.bn == 0) {
     const double ctas = over(a.N, 16) * over(a.M, 8 * f.by), bytes = ctas * a.K * (16.0 + 8 * f.by);
-    if (f.by == 1) return 1.7 + bytes / 7.1e6;
-    return 1.7 + (a.K >= 1024 && ctas <= 4 * sms ? over(a.K, 1024) * 0.25 : over(a.K, 256) * 0.16) + bytes / 9.0e6;
+    const bool ahead = a.K >= 1024 && ctas <= 4 * sms;
+    if (f.by == 1) return 1.3 + (ahead ? over(a.K, 2048) * 0.38 : 0.0) + bytes / 7.7e6;
+    return 1.3 + (ahead ? over(a.K, 1024) * 0.43 : over(a.K, 256) * 0.14) + bytes / 8.1e6;
   }
+  // 128-byte lines that 128 bytes of a row lie in, on average: rows are K bytes apart.
+  const uint32_t low = a.K & (0u - a.K);
+  const double lines = 2.0 - (low < 128 ? low : 128) / 128.0;
   if (f.bn == 256)
-    return 4.5 + std::ceil(over(a.M, 256) * over(a.N, 256) / (sms / 2)) * std::fmax(stages * 0.59, 1.2);
+    return 4.5 + std::ceil(over(a.M, 256) * over(a.N, 256) / (sms / 2)) * stages * 0.35 * (0.78 + 0.22 * lines);
   const double ctas = over(a.M, 128) * over(a.N, f.bn) * f.by, per_sm = std::ceil(ctas / int8_tile_slots(f.by));
   const double own = std::ceil(stages / f.by), rows = a.M < 128 ? over(a.M, 8) * 8 : 128;
-  const double pace = own * 0.34 * (per_sm == 1 ? 1 : per_sm * 0.65);  // two CTAs of an SM overlap
-  const double bytes = ctas * own * (rows + f.bn) * 128;
-  const double tail = f.by == 1 ? per_sm * (f.bn == 64 ? 0.67 : 3.4) : 1.8 + per_sm * 0.79 * (f.bn / 64);
-  return 2.1 + std::fmax(pace, bytes / 9.7e6) + tail;
+  // A stage takes its products or its lines through the SM's copy engine; two CTAs of
+  // an SM overlap.
+  const double stage = std::fmax(f.bn == 64 ? 0.17 : 0.18, (rows + f.bn) * lines * 0.63e-3);
+  const double pace = own * stage * (per_sm == 1 ? 1 : per_sm * 0.81);
+  const double bytes = ctas * own * (rows + f.bn) * 128, through = bytes / 17e6 * (0.53 + 0.47 * lines);
+  const double full = 0.5 + 0.5 * rows / 128;
+  const double tail = f.by == 1 ? per_sm * (f.bn == 64 ? 0.75 : 2.8) * full : 1.7 + per_sm * (f.bn / 64) * full;
+  return 2.1 + std::fmax(pace, through) + tail;
 }
 
 }  // namespace

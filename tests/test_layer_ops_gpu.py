@@ -470,7 +470,13 @@ FORMS = [(1, 1, 4480), (243, 1, 4384), (138, 8, 4480), (26, 288, 5264), (5, 3686
          (1717, 19, 4480), (1198, 34, 4464), (65, 774, 4000), (113, 639, 2880), (625, 184, 1888), (89, 960, 3936),
          (268, 4456, 1520), (140, 4991, 2608), (653, 2830, 1200),
          (17, 3874, 3216), (2866, 66, 1376), (1470, 131, 1408), (49, 3960, 1408), (72, 2651, 1472), (2260, 72, 2176),
-         (1431, 2413, 80), (2396, 1526, 80), (1832, 2008, 80), (1025, 2305, 2064), (511, 8191, 2048), (2091, 2259, 96)]
+         (1431, 2413, 80), (2396, 1526, 80), (1832, 2008, 80), (1025, 2305, 2064), (511, 8191, 2048), (2091, 2259, 96),
+         (153, 7921, 944), (243, 6941, 1424), (488, 2964, 2304), (1, 6934, 6096), (2, 7667, 5584), (9, 5993, 5040),
+         (1, 3989, 6016), (14, 2939, 6352), (2064, 71, 5504), (420, 8198, 64), (3988, 6446, 16), (474, 7623, 256),
+         (642, 1896, 128), (784, 1388, 224), (494, 4471, 208), (1, 7839, 2928), (63, 3679, 688), (1770, 181, 896),
+         (9, 4585, 3392), (2244, 79, 3120), (487, 729, 2320), (4989, 19, 6128), (9, 1568, 6384), (2137, 55, 1904),
+         (579, 250, 2336), (813, 18, 6016), (209, 190, 3904), (408, 98, 4912), (98, 67, 1024), (189, 2708, 48),
+         (16, 1008, 8192), (63, 1024, 1664)]
 
 
 @pytest.mark.parametrize("m,n,k", FORMS)
