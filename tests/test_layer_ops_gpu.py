@@ -4,6 +4,10 @@ Tolerances count roundings: a rounding to type t is off by at most finfo(t).eps 
 relative to the value (BF16 2^-8, FP32 2^-24, E4M3 2^-4).
 """
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -638,6 +642,36 @@ def test_block_captured_and_replayed(nvm):
     blocks[0].x.copy_(torch.randn_like(blocks[0].x))
     graphs[0].replay()
     blocks[0].check()
+
+
+FIRST_CALL_CAPTURED = """
+import torch
+import nvfp4_weight_quantized_moe_b200 as nvm
+g = torch.Generator(device="cuda").manual_seed(1)
+m, n, k = 256, 2048, 7168
+x = torch.randint(-127, 128, (m, k), dtype=torch.int8, device="cuda", generator=g)
+w = torch.randint(-127, 128, (n, k), dtype=torch.int8, device="cuda", generator=g)
+xs, ws, out = torch.rand(m, device="cuda"), torch.rand(n, device="cuda"), torch.zeros(m, n, device="cuda")
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    nvm.int8_matmul(x, xs, w, ws, out)
+graph.replay()
+torch.cuda.synchronize()
+captured = out.clone()
+nvm.int8_matmul(x, xs, w, ws, out)
+torch.cuda.synchronize()
+assert torch.equal(captured, out) and out.abs().max() > 0
+assert nvm.device_error() == 0
+print("captured")
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured(nvm):
+    """What a launch asks the device once (shared-memory limits, clusters) is asked during a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and "captured" in res.stdout, res.stderr[-2000:]
 
 
 def test_calls_on_two_streams_at_once(nvm):
