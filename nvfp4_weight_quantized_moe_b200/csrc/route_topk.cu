@@ -132,19 +132,20 @@ NVM_DEV bool in_mask(const RouteArgs& a, uint32_t mask, int e) {
   return ((mask >> ((uint32_t)e * a.group_magic >> 20)) & 1u) != 0;
 }
 
-// Lane g gets the key of the score of group g from `value`, the choice keys of the
-// lane's experts: of the best value, or of the sum of the best two (of the one,
-// where only one can be chosen).
+// A group's two best choice keys.
+template <typename Key>
+struct Best2 {
+  Key one, two;
+};
+
+// Lane g gets those of group g from `value`, the choice keys of the lane's experts;
+// the second one only where a group's score needs it.
 template <typename F, int EPL, typename Value>
-NVM_DEV typename KeyOf<F>::type group_scores(const RouteArgs& a, Value value) {
+NVM_DEV Best2<typename KeyOf<F>::type> best_two(const RouteArgs& a, Value value) {
   using Key = typename KeyOf<F>::type;
   constexpr int kUnroll = sizeof(F) == 4 ? EPL : 1;
-  constexpr Key kNone = KeyOf<F>::none;
   const int lane = threadIdx.x & 31, e0 = lane * a.per_lane;
-  auto total = [&](Key k1, Key k2) -> Key {
-    if (k1 <= kNone || k2 <= kNone || a.group_top < 2) return k1;
-    return order_key(key_value(k1, F()) + key_value(k2, F()));
-  };
+  Best2<Key> mine{0, 0};
   if (a.group_lanes > 0) {
     Key k1 = 0, k2 = 0;
 #pragma unroll kUnroll
@@ -160,10 +161,12 @@ NVM_DEV typename KeyOf<F>::type group_scores(const RouteArgs& a, Value value) {
       k1 = p1 > k1 ? p1 : k1;
       k2 = lower > second ? lower : second;
     }
-    const Key mine = __shfl_sync(kFull, total(k1, k2), lane * a.group_lanes & 31);
-    return lane < a.groups ? mine : 0;
+    const int from = lane * a.group_lanes & 31;
+    k1 = __shfl_sync(kFull, k1, from);
+    if (a.group_top > 1) k2 = __shfl_sync(kFull, k2, from);
+    if (lane < a.groups) mine = {k1, k2};
+    return mine;
   }
-  Key mine = 0;
 #pragma unroll 1
   for (int g = 0; g < a.groups; ++g) {
     Key k1 = 0, k2 = 0;  // this lane's best two
@@ -177,9 +180,26 @@ NVM_DEV typename KeyOf<F>::type group_scores(const RouteArgs& a, Value value) {
     const Key best = warp_max_key(k1);
     const unsigned at = __ballot_sync(kFull, k1 == best);
     const Key next = warp_max_key(lane == __ffs(at) - 1 ? k2 : k1);
-    if (lane == g) mine = total(best, next);
+    if (lane == g) mine = {best, next};
   }
   return mine;
+}
+
+// Whether a group's score is the sum of two values: it is that of the one where only
+// one can be chosen.
+template <typename F>
+NVM_DEV bool is_sum(const RouteArgs& a, Best2<typename KeyOf<F>::type> b) {
+  return a.group_top > 1 && b.two > KeyOf<F>::none;
+}
+
+// Key of a group's score.  Two values near the type's lowest add up to -infinity in
+// FP32; such a group can be chosen, so it counts as the lowest finite one (and is
+// ordered in FP64).
+NVM_DEV float finite_sum(float x, float y) { return fmaxf(x + y, -FLT_MAX); }
+NVM_DEV double finite_sum(double x, double y) { return x + y; }
+template <typename F>
+NVM_DEV typename KeyOf<F>::type group_key(const RouteArgs& a, Best2<typename KeyOf<F>::type> b) {
+  return is_sum<F>(a, b) ? order_key(finite_sum(key_value(b.one, F()), key_value(b.two, F()))) : b.one;
 }
 
 // The topk_groups best of the groups' keys, as a mask; a group's rank counts the
@@ -263,10 +283,10 @@ __device__ __noinline__ uint64_t choice_exactly(const RouteArgs& a, const T* row
 template <typename T, int EPL>
 __device__ __noinline__ unsigned groups_exactly(const RouteArgs& a, const T* row, Scores64 s) {
   const int e0 = (threadIdx.x & 31) * a.per_lane;
-  const uint64_t mine = group_scores<double, EPL>(a, [&](int j) -> uint64_t {
+  const Best2<uint64_t> two = best_two<double, EPL>(a, [&](int j) -> uint64_t {
     return j < a.per_lane && e0 + j < a.E ? choice_exactly<T>(a, row, s, e0 + j) : 0;
   });
-  return best_groups(a, mine, KeyOf<double>::none);
+  return best_groups(a, group_key<double>(a, two), KeyOf<double>::none);
 }
 
 // The whole choice among the experts of the groups of `mask`: topk times the best.
@@ -367,35 +387,45 @@ NVM_DEV void select_experts(const RouteArgs& a, const T* row, const float (&l)[E
   unsigned mask = 1u;
   if (a.groups > 1) {
     const bool sums = a.group_top > 1;
-    uint32_t mine;
+    Best2<uint32_t> two;
     if (scored || !sums) {
-      mine = group_scores<float, EPL>(a, [&](int j) -> uint32_t { return key[j]; });
+      two = best_two<float, EPL>(a, [&](int j) -> uint32_t { return key[j]; });
     } else {
-      mine = group_scores<float, EPL>(a, [&](int j) -> uint32_t {
+      two = best_two<float, EPL>(a, [&](int j) -> uint32_t {
         if (key[j] <= kNone) return 0;
         return order_key(a.softmax ? softmax_score(l[j]) : sigmoid_score(l[j]));
       });
     }
-    // The best groups one after another; then the worst kept stands against the
-    // best left out (there may be none).
-    mask = 0;
+    // A score is off by its values' errors and, for a sum, its own rounding: all of them
+    // by the values' sizes, which a sum of opposite signs does not show.
+    uint32_t rest = group_key<float>(a, two);
+    const float v = key_value(rest, 0.0f);
+    const bool sum = is_sum<float>(a, two);
+    const float size = fabsf(key_value(two.one, 0.0f)) + (sum ? fabsf(key_value(two.two, 0.0f)) : 0.0f);
+    const float off = ((sum ? unit : 0.5f * unit) + (sum ? size + fabsf(v) : size) * 0x1p-24f) * 0x1.00001p0f;
+    // The best groups one after another.
     uint32_t worst = 0;
+    mask = 0;
 #pragma unroll 1
     for (int r = 0; r < a.topk_groups; ++r) {
-      const uint32_t top = __reduce_max_sync(kFull, mine);
+      const uint32_t top = __reduce_max_sync(kFull, rest);
       if (top <= kNone) break;
-      const int at = __ffs(__ballot_sync(kFull, mine == top)) - 1;
+      const int at = __ffs(__ballot_sync(kFull, rest == top)) - 1;
       mask |= 1u << at;
-      if (lane == at) mine = 0;
+      if (lane == at) rest = 0;
       worst = top;
     }
+    // FP32 has settled it if the least that a kept group's score can be is above the most
+    // that a left one's can (there may be none), both as distances from the worst kept
+    // one's: exact where they are small (2^-20 in `off` covers the ends' rounding).  What is
+    // not finite may be anywhere.
     if (scored || sums) {
-      const uint32_t below = __reduce_max_sync(kFull, mine);
-      if (below > kNone) {
-        const float v = key_value(worst, 0.0f);
-        if (v - key_value(below, 0.0f) <= a.group_top * bound(v))
-          mask = groups_exactly<T, EPL>(a, row, scores_exactly<T>(a, row, lmax));
-      }
+      const float from = v - key_value(worst, 0.0f);
+      const bool bounded = off < INFINITY;
+      const uint32_t least = (mask >> lane) & 1u ? order_key(bounded ? from - off : -INFINITY) : 0xffffffffu;
+      const uint32_t most = rest > kNone ? order_key(bounded ? from + off : INFINITY) : 0u;
+      if (__reduce_min_sync(kFull, least) <= __reduce_max_sync(kFull, most))
+        mask = groups_exactly<T, EPL>(a, row, scores_exactly<T>(a, row, lmax));
     }
     if (a.group_lanes > 0) {
       const uint32_t stays = (mask >> (lane / a.group_lanes)) & 1u ? 0xffffffffu : 0u;
