@@ -621,8 +621,11 @@ NVFP4_MOE_API int nvfp4_moe_route_topk(const nvfp4_moe_route_args* args, cudaStr
  *                 [num_rows], or both NULL; at least one of out and q
  * residual_out and out may be exactly x or residual (same address, element size
  * and row distance); any other overlap is refused.  A row of zeros gives zeros
- * and a scale of 0.  A NaN or infinity in a row makes its y (not its r) and its
- * scale NaN; a row whose sum of squares passes the FP32 range gives zeros.
+ * and a scale of 0.  So does, in out, q and q_scale, a row of finite values whose
+ * sum of squares passes the FP32 range (one value of 2^64, or all of 2^57 at the
+ * longest hidden, is enough) while r * weight stays inside it.  A NaN in a row makes
+ * its y and its scale NaN; an infinity makes its scale NaN and its y NaN in its own
+ * place, 0 elsewhere.  The codes of such a row mean nothing; its residual_out is r.
  * ESHAPE: hidden not in 1..32768, ldx or ldr < hidden, num_rows >= 2^31.
  * EINVAL: unknown type, eps not a positive finite number, NULL or overlapping
  * pointers, q without q_scale or the other way round, residual_out without

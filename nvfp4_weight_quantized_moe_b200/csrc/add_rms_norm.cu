@@ -350,7 +350,8 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormArgs a) {
   }
   const float inv = rsqrtf(sum / (float)H + a.eps);
   const float range = a.q_kind == kQuantInt8 ? 127.0f : 448.0f;
-  const Step step = code_step(most, range);
+  // Squares past the FP32 range make the row's factor and scale 0, and so its codes.
+  const Step step = code_step(most, sum < INFINITY ? range : 0.0f);
   if (CODES && tid == 0) a.q_scale[row] = most * inv / range;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
