@@ -609,7 +609,12 @@ NVFP4_MOE_API int nvfp4_moe_route_topk(const nvfp4_moe_route_args* args, cudaStr
  *   q_scale = max|y| / Q, q = y / q_scale rounded to nearest even,
  *   Q = 127 (INT8) or 448 (E4M3)
  *
- * r, the mean and y are FP32; out and q are rounded once, from the unrounded r.
+ * r, the sum of squares and y are FP32, from the unrounded sum's FP32 r and not from
+ * residual_out.  A code is not formed from the rounded y: the row's root cancels in
+ * y / q_scale, so it is r * weight * (Q / max|r * weight|), each step rounded to FP32
+ * (r, two products, the quotient) before the code's own rounding.  That is as near
+ * to the exact quotient as dividing an FP32 y by an FP32 scale; a value within a few
+ * 2^-24 of the middle between two codes may get either.
  *
  * Arguments (a HOST struct, read during the call):
  *   x             bf16 or f32 [num_rows, hidden], rows ldx elements apart
@@ -664,8 +669,9 @@ NVFP4_MOE_API int nvfp4_moe_add_rms_norm(const nvfp4_moe_norm_args* args, cudaSt
  *   w_scale  f32 [n]        bias  f32 [n] or NULL
  *   out      bf16 or f32 (out_type) [num_tokens, n], rows ldo elements apart
  *
- * The integer sums are exact, so the result does not depend on how the work is
- * split; scales and bias are applied in FP32 and the result is rounded once.
+ * The integer sums are exact.  Then, each step rounded to FP32: the sum (exact below
+ * 2^24), times x_scale, times w_scale, plus bias; and the result to out_type.  The
+ * same steps for every size, so a token's row has the same bits in any batch.
  * ESHAPE: k not a multiple of 16 in 16..131056, ldx < k or not a multiple of
  * 16, ldo < n, n == 0.  EINVAL: unknown type, NULL or misaligned pointers, out
  * overlapping an input.

@@ -3,8 +3,9 @@
 //   out[m, n] = x_scale[m] * w_scale[n] * sum_k x[m, k] w[n, k]  (+ bias[n])
 //
 // The sums are exact in 32-bit integers (K is bounded so that they cannot
-// overflow), so every split of K gives the same bits; scales and bias are
-// applied in FP32 and the result is rounded once to the output's type.
+// overflow), so every split of K gives the same bits; the sum, the two products
+// with the scales and the addition of the bias are rounded to FP32 each
+// (int8_scaled, the same in all kernels), then the result to the output's type.
 //
 // Small batches take the register-fed kernel of this file, larger ones the
 // tensor-core kernels of int8_matmul_tc.cu (launch_int8_matmul has the rule).
@@ -21,6 +22,7 @@
 #include <cmath>
 
 #include "common.cuh"
+#include "int8_epilogue.cuh"
 #include "kernels.h"
 
 namespace nvm {
@@ -37,8 +39,6 @@ NVM_DEV void mma_s8_16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, ui
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-NVM_DEV float scaled(int sum, float xs, float ws) { return (float)sum * xs * ws; }
 
 NVM_DEV void store_out(void* out, bool f32, uint64_t at, float v) {
   if (f32) {
@@ -117,8 +117,8 @@ __global__ void __launch_bounds__(32 * WARPS) int8_matmul_reg_kernel(const Int8M
     int sum = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) sum += part[w][i / kRegRows][i % kRegRows];
-    float v = scaled(sum, a.x_scale[m], a.w_scale[n]);
-    if (a.bias != nullptr) v += a.bias[n];
+    float v = int8_scaled(sum, a.x_scale[m], a.w_scale[n]);
+    if (a.bias != nullptr) v = int8_biased(v, a.bias[n]);
     store_out(a.out, a.out_f32, (uint64_t)m * a.ldo + n, v);
   }
 }

@@ -35,6 +35,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "int8_epilogue.cuh"
 #include "kernels.h"
 #include "tc_common.cuh"
 #include "tensor_map.h"
@@ -45,8 +46,6 @@ namespace {
 
 constexpr int kStageK = 128;   // bytes of K per stage: one swizzled row
 constexpr int kTileM = 128;
-
-NVM_DEV float scaled(int sum, float xs, float ws) { return (float)sum * xs * ws; }
 
 NVM_DEV uint32_t bf16_pair(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -79,14 +78,14 @@ NVM_DEV void drain_rows(uint32_t taddr, int cols, uint8_t* stage, const float* w
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
         const float4 w4 = *reinterpret_cast<const float4*>(ws + c0 + 32 * h + j);
-        v[j] = scaled((int)d[j], xs, w4.x);
-        v[j + 1] = scaled((int)d[j + 1], xs, w4.y);
-        v[j + 2] = scaled((int)d[j + 2], xs, w4.z);
-        v[j + 3] = scaled((int)d[j + 3], xs, w4.w);
+        v[j] = int8_scaled((int)d[j], xs, w4.x);
+        v[j + 1] = int8_scaled((int)d[j + 1], xs, w4.y);
+        v[j + 2] = int8_scaled((int)d[j + 2], xs, w4.z);
+        v[j + 3] = int8_scaled((int)d[j + 3], xs, w4.w);
       }
       if (a.bias != nullptr) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += bias[c0 + 32 * h + j];
+        for (int j = 0; j < 32; ++j) v[j] = int8_biased(v[j], bias[c0 + 32 * h + j]);
       }
 #pragma unroll
       for (int p = 0; p < 32 / kPer; ++p) {
@@ -384,10 +383,11 @@ __global__ void __launch_bounds__(kTileThreads)
       }
       const float xs = scales[r];
       const float4 ws = *reinterpret_cast<const float4*>(scales + kTileM + c);
-      float4 v = make_float4(scaled(s.x, xs, ws.x), scaled(s.y, xs, ws.y), scaled(s.z, xs, ws.z), scaled(s.w, xs, ws.w));
+      float4 v = make_float4(int8_scaled(s.x, xs, ws.x), int8_scaled(s.y, xs, ws.y), int8_scaled(s.z, xs, ws.z),
+                             int8_scaled(s.w, xs, ws.w));
       if (a.bias != nullptr) {
         const float4 b = *reinterpret_cast<const float4*>(scales + kTileM + BN + c);
-        v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+        v = make_float4(int8_biased(v.x, b.x), int8_biased(v.y, b.y), int8_biased(v.z, b.z), int8_biased(v.w, b.w));
       }
       const uint64_t o = (uint64_t)m * a.ldo + n;
       if (a.out_f32) {

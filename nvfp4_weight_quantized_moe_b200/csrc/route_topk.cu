@@ -599,7 +599,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, EPL <= 8 ? 8 : EPL == 16 ? 6 :
 
   // Weights.  Renormalised ones are formed relative to the largest chosen
   // logit, so they are never 0 / 0: softmax exp(l - top); sigmoid
-  // exp(l - base) / (1 + exp(l)) with base = min(0, top).
+  // exp(l - base) / (1 + exp(l)) with base = min(0, top).  In FP32: a difference, one or
+  // two exponentials and quotients of at most 2 ulp, the sum and two products; the
+  // weights scale FP32 expert outputs, which carry larger errors.
   const int id = picks.id[lane];
   float x = -INFINITY;
   if (id >= 0) x = a.bias == nullptr ? picks.logit[lane] : clean_logit(logit_f32<T>(__ldg(row + id)));
