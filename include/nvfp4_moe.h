@@ -693,6 +693,15 @@ typedef struct {
 
 NVFP4_MOE_API int nvfp4_moe_int8_matmul(const nvfp4_moe_int8_args* args, cudaStream_t stream);
 
+/*
+ * Host helper: the kernel that nvfp4_moe_int8_matmul takes for these sizes on the
+ * current device (all give the same bits), for logs and tests.  form[4], host:
+ * channels of a tile (16 register-fed, 64 or 128 on the tensor cores, 256 by pairs of
+ * CTAs), tokens of a tile, CTAs that split k (1, 2, 4, 8), and 1 for the variant with
+ * more loads in flight per SM.  ESHAPE: sizes that the product refuses, no tokens.
+ */
+NVFP4_MOE_API int nvfp4_moe_int8_form(uint32_t num_tokens, uint32_t n, uint32_t k, uint32_t form[4]);
+
 /* Host helper: launch bound on active experts, min(num_experts, num_pairs). */
 NVFP4_MOE_API uint32_t nvfp4_moe_active_cap(uint32_t num_experts, uint32_t num_pairs);
 

@@ -32,6 +32,7 @@ from ._binding import (  # noqa: F401
     forward_nongated,
     gate_up_silu,
     gate_up_silu_ws,
+    int8_form,
     int8_matmul,
     route_sort,
     route_topk,

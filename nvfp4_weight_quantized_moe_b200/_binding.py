@@ -119,6 +119,7 @@ _sig = {
     "nvfp4_moe_route_topk": (c_int, [ctypes.c_char_p, c_void_p]),
     "nvfp4_moe_add_rms_norm": (c_int, [ctypes.c_char_p, c_void_p]),
     "nvfp4_moe_int8_matmul": (c_int, [ctypes.c_char_p, c_void_p]),
+    "nvfp4_moe_int8_form": (c_int, [c_u32, c_u32, c_u32, ctypes.POINTER(c_u32)]),
     "nvfp4_moe_workspace_bytes": (ctypes.c_size_t, [c_u32, c_u32, c_u32, c_u32]),
     "nvfp4_moe_device_error": (c_int, [c_int]),
     "nvfp4_moe_wait_selftest": (c_int, [c_u32, c_int, c_void_p]),
@@ -626,3 +627,14 @@ def int8_matmul(x_q, x_scale, w_q, w_scale, out, *, bias=None, stream=None) -> N
     b = 0 if bias is None else _vector(bias, n, dev, "bias")
     _launch("nvfp4_moe_int8_matmul", _INT8_ARGS,
             (x, xs, w, ws, b, _on(out, dev, "out"), ldx, ldo, m, n, k, kind), dev, stream)
+
+
+def int8_form(num_tokens: int, n: int, k: int) -> dict:
+    """nvfp4_moe_int8_form: the kernel that :func:`int8_matmul` takes for these sizes on the
+    current device, as ``channels`` and ``tokens`` of a tile, ``split`` (CTAs that share a
+    tile's k) and ``deep`` (the variant with more loads in flight)."""
+    if not all(0 <= v <= 0xffffffff for v in (num_tokens, n, k)):
+        raise ValueError("sizes out of range")
+    form = (c_u32 * 4)()
+    _check("nvfp4_moe_int8_form", _lib.nvfp4_moe_int8_form(num_tokens, n, k, form))
+    return dict(channels=form[0], tokens=form[1], split=form[2], deep=bool(form[3]))

@@ -657,6 +657,10 @@ bool float_type(int t) { return t == NVFP4_MOE_BF16 || t == NVFP4_MOE_F32; }
 
 uint64_t float_bytes(int t) { return t == NVFP4_MOE_F32 ? 4 : 2; }
 
+bool int8_sizes(uint32_t tokens, uint32_t n, uint32_t k) {
+  return tokens <= 0x7fffff00u && n != 0 && n <= 0x7fffff00u && k != 0 && k % 16 == 0 && k <= kMaxInt8K;
+}
+
 }  // namespace
 
 int nvfp4_moe_route_topk(const nvfp4_moe_route_args* r, cudaStream_t stream) {
@@ -761,8 +765,8 @@ int nvfp4_moe_int8_matmul(const nvfp4_moe_int8_args* args, cudaStream_t stream) 
   if (args == nullptr) return NVFP4_MOE_EINVAL;
   const nvfp4_moe_int8_args& g = *args;
   if (!float_type(g.out_type)) return NVFP4_MOE_EINVAL;
-  if (g.n == 0 || g.n > 0x7fffff00u || g.num_tokens > 0x7fffff00u || g.k == 0 || g.k % 16 != 0 || g.k > kMaxInt8K ||
-      g.ldx < g.k || g.ldx % 16 != 0 || g.ldx > kMaxPitch || g.ldo < g.n || g.ldo > kMaxPitch)
+  if (!int8_sizes(g.num_tokens, g.n, g.k) || g.ldx < g.k || g.ldx % 16 != 0 || g.ldx > kMaxPitch || g.ldo < g.n ||
+      g.ldo > kMaxPitch)
     return NVFP4_MOE_ESHAPE;
   if (g.num_tokens == 0) return NVFP4_MOE_OK;
   if (g.x == nullptr || g.x_scale == nullptr || g.w == nullptr || g.w_scale == nullptr || g.out == nullptr)
@@ -793,6 +797,17 @@ int nvfp4_moe_int8_matmul(const nvfp4_moe_int8_args* args, cudaStream_t stream) 
   a.K = g.k;
   a.out_f32 = g.out_type == NVFP4_MOE_F32;
   return status_of(launch_int8_matmul(a, stream));
+}
+
+int nvfp4_moe_int8_form(uint32_t num_tokens, uint32_t n, uint32_t k, uint32_t form[4]) {
+  if (form == nullptr) return NVFP4_MOE_EINVAL;
+  if (num_tokens == 0 || !int8_sizes(num_tokens, n, k)) return NVFP4_MOE_ESHAPE;
+  const Int8Form f = int8_form(num_tokens, n, k);
+  form[0] = f.channels;
+  form[1] = f.tokens;
+  form[2] = f.split;
+  form[3] = f.deep ? 1 : 0;
+  return NVFP4_MOE_OK;
 }
 
 }  // extern "C"

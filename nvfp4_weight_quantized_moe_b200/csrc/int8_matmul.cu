@@ -130,22 +130,23 @@ cudaError_t launch_reg_of(const Int8MatmulArgs& a, uint64_t blocks, cudaStream_t
   return launch_pdl(int8_matmul_reg_kernel<TT, WARPS, AHEAD>, dim3((unsigned)blocks), dim3(32 * WARPS), 0, stream, a);
 }
 
-template <int TT>
-cudaError_t launch_reg(const Int8MatmulArgs& a, cudaStream_t stream) {
-  const uint64_t blocks = (uint64_t)((a.N + kRegRows - 1) / kRegRows) * ((a.M + 8 * TT - 1) / (8 * TT));
-  if (blocks > 0x7fffffffull) return cudaErrorInvalidConfiguration;
-  // A long K is a chain of round trips to memory: eight warps with as many chunks in
-  // flight as registers allow (1 token, n = k = 4096: 3.6 us, with four warps and one
-  // chunk 7.1).  A short one, or more CTAs than keep every SM busy, is better off
-  // with small CTAs (246 x 336 x 192: 2.1 us against 4.0).
-  constexpr int kLong = TT == 1 ? 4 : 2;
-  if (a.K >= 1024 && blocks <= 4ull * sm_count()) return launch_reg_of<TT, 8, kLong>(a, blocks, stream);
-  return launch_reg_of<TT, 4, 1>(a, blocks, stream);
+uint64_t reg_blocks(uint32_t M, uint32_t N, uint32_t tiles) {
+  return (uint64_t)((N + kRegRows - 1) / kRegRows) * ((M + 8 * tiles - 1) / (8 * tiles));
 }
 
-}  // namespace
+// A long K is a chain of round trips to memory: eight warps with as many chunks in
+// flight as registers allow (1 token, n = k = 4096: 3.6 us, with four warps and one
+// chunk 7.1; weights in the L2).  A short one, or more CTAs than keep every SM busy,
+// is better off with small CTAs (246 x 336 x 192: 2.1 us against 4.0).
+bool reg_deep(uint64_t blocks, uint32_t K, int sms) { return K >= 1024 && blocks <= 4ull * sms; }
 
-namespace {
+template <int TT>
+cudaError_t launch_reg(const Int8MatmulArgs& a, bool deep, cudaStream_t stream) {
+  const uint64_t blocks = reg_blocks(a.M, a.N, TT);
+  if (blocks > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+  constexpr int kLong = TT == 1 ? 4 : 2;
+  return deep ? launch_reg_of<TT, 8, kLong>(a, blocks, stream) : launch_reg_of<TT, 4, 1>(a, blocks, stream);
+}
 
 // Which kernel takes a product: the shortest of the estimated times below, in
 // microseconds.  Their forms follow the kernels (rounds of CTAs, a pace per
@@ -158,22 +159,23 @@ struct Form {
   uint32_t by;  // register-fed: 8-token tiles; tiles: CTAs that split K
 };
 
-double estimate(const Int8MatmulArgs& a, Form f, int sms) {
+double estimate(uint32_t M, uint32_t N, uint32_t K, Form f, int sms) {
   auto over = [](uint64_t x, uint64_t y) { return (double)((x + y - 1) / y); };
-  const double stages = over(a.K, 128);
+  const double stages = over(K, 128);
   if (f.bn == 0) {
-    const double ctas = over(a.N, 16) * over(a.M, 8 * f.by), bytes = ctas * a.K * (16.0 + 8 * f.by);
-    const bool ahead = a.K >= 1024 && ctas <= 4 * sms;
-    if (f.by == 1) return 1.3 + (ahead ? over(a.K, 2048) * 0.38 : 0.0) + bytes / 7.7e6;
-    return 1.3 + (ahead ? over(a.K, 1024) * 0.43 : over(a.K, 256) * 0.14) + bytes / 8.1e6;
+    const uint64_t ctas = reg_blocks(M, N, f.by);
+    const double bytes = (double)ctas * K * (16.0 + 8 * f.by);
+    const bool deep = reg_deep(ctas, K, sms);
+    if (f.by == 1) return 1.3 + (deep ? over(K, 2048) * 0.38 : 0.0) + bytes / 7.7e6;
+    return 1.3 + (deep ? over(K, 1024) * 0.43 : over(K, 256) * 0.14) + bytes / 8.1e6;
   }
   // 128-byte lines that 128 bytes of a row lie in, on average: rows are K bytes apart.
-  const uint32_t low = a.K & (0u - a.K);
+  const uint32_t low = K & (0u - K);
   const double lines = 2.0 - (low < 128 ? low : 128) / 128.0;
   if (f.bn == 256)
-    return 4.5 + std::ceil(over(a.M, 256) * over(a.N, 256) / (sms / 2)) * stages * 0.35 * (0.78 + 0.22 * lines);
-  const double ctas = over(a.M, 128) * over(a.N, f.bn) * f.by, per_sm = std::ceil(ctas / int8_tile_slots(f.by));
-  const double own = std::ceil(stages / f.by), rows = a.M < 128 ? over(a.M, 8) * 8 : 128;
+    return 4.5 + std::ceil(over(M, 256) * over(N, 256) / (sms / 2)) * stages * 0.35 * (0.78 + 0.22 * lines);
+  const double ctas = over(M, 128) * over(N, f.bn) * f.by, per_sm = std::ceil(ctas / int8_tile_slots(f.by));
+  const double own = std::ceil(stages / f.by), rows = M < 128 ? over(M, 8) * 8 : 128;
   // A stage takes its products or its lines through the SM's copy engine; two CTAs of
   // an SM overlap.
   const double stage = std::fmax(f.bn == 64 ? 0.17 : 0.18, (rows + f.bn) * lines * 0.63e-3);
@@ -186,22 +188,29 @@ double estimate(const Int8MatmulArgs& a, Form f, int sms) {
 
 }  // namespace
 
-cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, cudaStream_t stream) {
+Int8Form int8_form(uint32_t M, uint32_t N, uint32_t K) {
   static constexpr Form kForms[] = {{0, 1}, {0, 2}, {64, 1}, {64, 2}, {64, 4}, {64, 8}, {128, 1}, {128, 4}, {256, 1}};
   const int sms = sm_count();
   Form best = kForms[0];
-  double least = estimate(a, best, sms);
+  double least = estimate(M, N, K, best, sms);
   for (const Form& f : kForms) {
-    if (f.bn > 0 && f.by > (a.K + 127) / 128) continue;  // a stage of K for each CTA at least
-    const double t = estimate(a, f, sms);
+    if (f.bn > 0 && f.by > (K + 127) / 128) continue;  // a stage of K for each CTA at least
+    const double t = estimate(M, N, K, f, sms);
     if (t < least) {
       least = t;
       best = f;
     }
   }
-  if (best.bn == 0) return best.by == 1 ? launch_reg<1>(a, stream) : launch_reg<2>(a, stream);
-  if (best.bn == 256) return launch_int8_pair(a, stream);
-  return launch_int8_tile(a, best.bn, best.by, stream);
+  if (best.bn == 0) return {(uint32_t)kRegRows, 8 * best.by, 1, reg_deep(reg_blocks(M, N, best.by), K, sms)};
+  if (best.bn == 256) return {256, 256, 1, true};
+  return {(uint32_t)best.bn, 128, best.by, int8_tile_deep(M, N, best.bn, best.by)};
+}
+
+cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, cudaStream_t stream) {
+  const Int8Form f = int8_form(a.M, a.N, a.K);
+  if (f.channels == 256) return launch_int8_pair(a, stream);
+  if (f.channels >= 64) return launch_int8_tile(a, f, stream);
+  return f.tokens == 8 ? launch_reg<1>(a, f.deep, stream) : launch_reg<2>(a, f.deep, stream);
 }
 
 }  // namespace nvm

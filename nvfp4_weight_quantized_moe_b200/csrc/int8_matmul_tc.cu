@@ -683,11 +683,15 @@ int int8_tile_slots(uint32_t split) {
   return clusters * (int)split;
 }
 
-cudaError_t launch_int8_tile(const Int8MatmulArgs& a, int bn, uint32_t split, cudaStream_t stream) {
-  const uint64_t ctas = (uint64_t)((a.M + kTileM - 1) / kTileM) * ((a.N + bn - 1) / bn) * split;
-  const bool deep = ctas <= (uint64_t)int8_tile_slots(split);
-  if (bn == 64) return deep ? launch_tile<64, true>(a, split, stream) : launch_tile<64, false>(a, split, stream);
-  return deep ? launch_tile<128, true>(a, split, stream) : launch_tile<128, false>(a, split, stream);
+bool int8_tile_deep(uint32_t M, uint32_t N, uint32_t bn, uint32_t split) {
+  const uint64_t ctas = (uint64_t)((M + kTileM - 1) / kTileM) * ((N + bn - 1) / bn) * split;
+  return ctas <= (uint64_t)int8_tile_slots(split);
+}
+
+cudaError_t launch_int8_tile(const Int8MatmulArgs& a, const Int8Form& f, cudaStream_t stream) {
+  if (f.channels == 64)
+    return f.deep ? launch_tile<64, true>(a, f.split, stream) : launch_tile<64, false>(a, f.split, stream);
+  return f.deep ? launch_tile<128, true>(a, f.split, stream) : launch_tile<128, false>(a, f.split, stream);
 }
 
 cudaError_t read_int8_error(int* value, bool clear) { return read_error_word(&g_device_error, value, clear); }

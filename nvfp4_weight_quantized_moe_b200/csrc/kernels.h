@@ -160,9 +160,18 @@ struct Int8MatmulArgs {
   bool out_f32;
 };
 cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, cudaStream_t stream);
-// Its tensor-core forms (int8_matmul_tc.cu): 128 x bn tiles (bn 64 or 128) with K
-// split over a cluster of `split` CTAs (1, 2, 4, 8); 256 x 256 tiles by CTA pairs.
-cudaError_t launch_int8_tile(const Int8MatmulArgs& a, int bn, uint32_t split, cudaStream_t stream);
+// The kernel that it takes for these sizes on the current device: register-fed tiles of
+// 16 channels and 8 or 16 tokens; tensor-core tiles (int8_matmul_tc.cu) of 64 or 128
+// channels and 128 tokens with K split over a cluster of `split` CTAs (1, 2, 4, 8; of 128
+// channels 1, 4), or of 256 x 256 by CTA pairs.  deep: eight warps with more chunks in
+// flight; a ring that takes the SM.
+struct Int8Form {
+  uint32_t channels, tokens, split;
+  bool deep;
+};
+Int8Form int8_form(uint32_t M, uint32_t N, uint32_t K);
+cudaError_t launch_int8_tile(const Int8MatmulArgs& a, const Int8Form& f, cudaStream_t stream);
+bool int8_tile_deep(uint32_t M, uint32_t N, uint32_t bn, uint32_t split);
 // SMs that clusters of `split` CTAs can fill with one CTA each on the current device: a
 // cluster stays in one GPC, whose SMs are no multiple of 4 or 8 (a 16th cluster of eight
 // waited for a second round: 20 x 1008 x 8192 9.0 us, with two CTAs to an SM 5.9).

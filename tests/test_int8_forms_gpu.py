@@ -1,6 +1,9 @@
 """The int8 product's kernels, bit for bit: exact integer sums, then the header's FP32
 steps, whichever kernel takes the sizes."""
 
+import math
+import random
+
 import pytest
 import torch
 
@@ -55,3 +58,42 @@ def test_a_row_has_the_same_bits_in_any_batch(nvm):
         part = torch.empty(m, 1536, device="cuda")
         nvm.int8_matmul(x[:m], xs[:m], w, ws, part, bias=bias)
         assert torch.equal(part, whole[:m])
+
+
+# (channels, tokens, split, deep) of every kernel and cluster size that a product can take.
+VARIANTS = [(16, 8, 1, False), (16, 8, 1, True), (16, 16, 1, False), (16, 16, 1, True),
+            (64, 128, 1, False), (64, 128, 1, True), (64, 128, 2, True), (64, 128, 4, False), (64, 128, 4, True),
+            (64, 128, 8, False), (64, 128, 8, True), (128, 128, 1, False), (128, 128, 1, True),
+            (128, 128, 4, False), (128, 128, 4, True), (256, 256, 1, True)]
+
+
+@pytest.fixture(scope="module")
+def shapes(nvm):
+    """Up to three shapes for each variant that the choice takes on this device, small ones
+    first, from sizes spread over their logarithms."""
+    rng = random.Random(5)
+    size = lambda lo, hi: int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))  # noqa: E731
+    found = {}
+    for _ in range(150000):
+        shape = (size(1, 8192), size(1, 8192), 16 * size(1, 512))
+        if math.prod(shape) < 5e10:
+            found.setdefault(tuple(nvm.int8_form(*shape).values()), []).append(shape)
+    return {v: sorted(s, key=math.prod)[:: max(1, len(s) // 3)][:3] for v, s in found.items()}
+
+
+def test_the_choice_takes_every_variant_and_no_other(shapes):
+    assert set(shapes) == set(VARIANTS)
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+def test_every_variant_gives_the_same_steps(nvm, shapes, variant):
+    for m, n, k in shapes[variant]:
+        x, xs, w, ws, bias = _problem(m, n, k)
+        want = _steps(x, xs, w, ws) + bias
+        for dtype in (F32, BF16):
+            store = torch.full((m, n + 13), -7.0, dtype=dtype, device="cuda")
+            for out in (store[:, :n].clone(), store[:, 5:5 + n]):
+                nvm.int8_matmul(x, xs, w, ws, out, bias=bias)
+                assert torch.equal(out, want.to(dtype)), (m, n, k)
+            assert bool((store[:, :5] == -7.0).all()) and bool((store[:, 5 + n:] == -7.0).all())
+    assert nvm.device_error() == 0
