@@ -414,9 +414,12 @@ __global__ void __launch_bounds__(kTileThreads)
       }
     }
   };
-  if (split == 2) sum_rows(std::integral_constant<uint32_t, 2>());
-  else if (split == 4) sum_rows(std::integral_constant<uint32_t, 4>());
-  else sum_rows(std::integral_constant<uint32_t, 8>());
+  // Tiles of 128 channels are split over four CTAs only.
+  if constexpr (BN == 64) {
+    if (split == 2) sum_rows(std::integral_constant<uint32_t, 2>());
+    if (split == 8) sum_rows(std::integral_constant<uint32_t, 8>());
+  }
+  if (split == 4) sum_rows(std::integral_constant<uint32_t, 4>());
   // A CTA's sums stay until every CTA of its cluster has read them.
   cluster_sync();
 }
