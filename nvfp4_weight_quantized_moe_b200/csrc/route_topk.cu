@@ -639,9 +639,9 @@ namespace {
 
 template <typename T>
 cudaError_t launch_route_topk_of(const RouteArgs& a, cudaStream_t stream) {
-  // One warp per CTA while that leaves every SM at most a few tokens (their
-  // chains then run on separate schedulers), four for large batches.
-  const int warps = a.M <= 592 ? 1 : kMaxWarps;
+  // One warp per CTA while that leaves every SM at most four tokens, one for each of its
+  // schedulers; four for larger batches.
+  const int warps = a.M <= 4u * (uint32_t)sm_count() ? 1 : kMaxWarps;
   const dim3 grid((a.M + warps - 1) / warps), block(32 * warps);
   const int epl = a.per_lane;
   if (epl <= 1) return launch_pdl(route_topk_kernel<T, 1>, grid, block, 0, stream, a);
