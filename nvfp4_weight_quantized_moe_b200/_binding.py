@@ -11,11 +11,15 @@ the import fails.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import struct
+import warnings
 from typing import Optional
 
 import torch
+
+from .build import quick_call_path
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG_DIR, "libnvfp4moe.so")
@@ -26,12 +30,25 @@ if not os.path.exists(LIB_PATH):
         "(nvcc, sm_100a). There is no CPU fallback.")
 
 _lib = ctypes.CDLL(LIB_PATH)
-try:
-    from . import _quick_call
-except ImportError as e:
-    raise ImportError(
-        f"the binding's C++ part does not load ({e}): build it with "
-        "`python nvfp4_weight_quantized_moe_b200/build.py` against the installed PyTorch") from e
+
+
+def _load_quick_call():
+    """The binding's C++ part for the installed PyTorch, or None: every call then goes
+    through ctypes, with the same checks and results."""
+    path = quick_call_path(torch.__version__)
+    try:
+        spec = importlib.util.spec_from_file_location(__package__ + "._quick_call", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        return module
+    except ImportError as e:  # not built, or it does not load
+        warnings.warn(f"the binding's C++ part does not load ({e}): route_topk, add_rms_norm and int8_matmul take "
+                      "about 5 us longer from Python; `python nvfp4_weight_quantized_moe_b200/build.py --force` "
+                      "builds it against the installed PyTorch", RuntimeWarning, stacklevel=2)
+        return None
+
+
+_quick_call = _load_quick_call()
 
 c_void_p = ctypes.c_void_p
 c_u32 = ctypes.c_uint32
@@ -473,8 +490,9 @@ def forward_nongated(x, topk_ids, topk_weights, up: ExpertTables, down: ExpertTa
 _ROUTE_ARGS = struct.Struct("PPPPQIIIIIIiiif")   # nvfp4_moe_route_args
 _NORM_ARGS = struct.Struct("PPPPPPPQQIIiiiif")   # nvfp4_moe_norm_args
 _INT8_ARGS = struct.Struct("PPPPPPQQIIIi")       # nvfp4_moe_int8_args
-_quick_call.bind(*(ctypes.cast(getattr(_lib, f), c_void_p).value for f in (
-    "nvfp4_moe_route_topk", "nvfp4_moe_add_rms_norm", "nvfp4_moe_int8_matmul")))
+if _quick_call is not None:
+    _quick_call.bind(*(ctypes.cast(getattr(_lib, f), c_void_p).value for f in (
+        "nvfp4_moe_route_topk", "nvfp4_moe_add_rms_norm", "nvfp4_moe_int8_matmul")))
 
 
 def _rows(t: torch.Tensor, name: str):
@@ -544,7 +562,7 @@ def route_topk(logits, topk_ids, topk_weights, *, score="softmax", bias=None, nu
     code = SCORES.get(score)
     if code is None:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
-    if stream is None:
+    if stream is None and _quick_call is not None:
         status = _quick_call.route_topk(logits, topk_ids, topk_weights, bias, code, num_groups, topk_groups,
                                         group_top, renormalize, scale)
         if status >= 0:
@@ -571,7 +589,7 @@ def add_rms_norm(x, weight, eps, *, out=None, residual=None, residual_out=None, 
     residual's type), ``out`` (y in bf16), ``q`` with ``q_scale`` (y in int8 or
     float8_e4m3fn codes, one f32 scale per row).  ``residual_out`` may be
     ``residual`` itself."""
-    if stream is None:
+    if stream is None and _quick_call is not None:
         status = _quick_call.add_rms_norm(x, weight, eps, out, residual, residual_out, q, q_scale)
         if status >= 0:
             return _check("nvfp4_moe_add_rms_norm", status)
@@ -608,7 +626,7 @@ def int8_matmul(x_q, x_scale, w_q, w_scale, out, *, bias=None, stream=None) -> N
     ``x_q`` int8 [M, K] (rows may be strided), ``w_q`` int8 [N, K], f32 scales [M] and
     [N], f32 ``bias`` [N] or None, ``out`` bf16 or f32 [M, N] (rows may be strided).
     K is a multiple of 16; the integer sums are exact."""
-    if stream is None:
+    if stream is None and _quick_call is not None:
         status = _quick_call.int8_matmul(x_q, x_scale, w_q, w_scale, out, bias)
         if status >= 0:
             return _check("nvfp4_moe_int8_matmul", status)

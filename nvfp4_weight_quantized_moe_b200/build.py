@@ -1,5 +1,6 @@
 """Build the sm_100a shared library ``libnvfp4moe.so`` in-tree with nvcc, and the
 binding's small C++ part (``_quick_call``, against the installed PyTorch) with g++.
+The library needs nvcc alone; without the C++ part the binding works through ctypes.
 
     python nvfp4_weight_quantized_moe_b200/build.py [--verbose-ptxas] [--force]
 
@@ -27,7 +28,6 @@ LIB_NAME = "libnvfp4moe.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 QUICK_SRC = os.path.join(CSRC, "quick_call.cpp")
-QUICK_PATH = os.path.join(PKG_DIR, "_quick_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -52,30 +52,45 @@ def needs_build() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def quick_call_path(torch_version: str) -> str:
+    """Where the C++ part for this Python and that PyTorch lies: another version's, whose
+    classes may be laid out differently, has another name and is not loaded."""
+    return os.path.join(PKG_DIR, f"_quick_call.torch-{torch_version}" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
 def build_quick_call(force: bool = False) -> str:
     """The binding's C++ part: the tensors' checks and the call without ctypes."""
-    deps = [QUICK_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(QUICK_PATH) and all(
-            os.path.getmtime(d) <= os.path.getmtime(QUICK_PATH) for d in deps):
-        return QUICK_PATH
     import torch
+    path = quick_call_path(torch.__version__)
+    deps = [QUICK_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps):
+        return path
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(cuda, "include"),
-           "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE, "-o", QUICK_PATH + ".tmp", QUICK_SRC,
+           "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE, "-o", path + ".tmp", QUICK_SRC,
            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError(f"g++ failed with exit code {res.returncode}")
-    os.replace(QUICK_PATH + ".tmp", QUICK_PATH)
-    return QUICK_PATH
+    os.replace(path + ".tmp", path)
+    return path
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    build_quick_call(force)
+    """The library, and the binding's C++ part where its tools are there."""
+    path = build_library(force, verbose_ptxas)
+    try:
+        build_quick_call(force)
+    except (ImportError, OSError, RuntimeError) as e:  # no PyTorch, no g++, no headers
+        sys.stderr.write(f"the binding's C++ part is not built ({e}): its calls go through ctypes\n")
+    return path
+
+
+def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and not verbose_ptxas and not needs_build():
         return LIB_PATH
     cmd = [
