@@ -379,8 +379,11 @@ class NVFP4MoE:
         if m > bufs.num_tokens:
             raise ValueError("buffers were sized for fewer tokens")
         ids, weights = bufs.routed_ids[:m], bufs.routed_weights[:m]
-        router.route(logits, ids, weights, stream=stream)
-        return self.forward(x, ids, weights, bufs, stream=stream, **options)
+        # Both on one stream: the routing takes the device of its tensors, the forward the
+        # current one.
+        with torch.cuda.device(x.device):
+            router.route(logits, ids, weights, stream=stream)
+            return self.forward(x, ids, weights, bufs, stream=stream, **options)
 
     def _forward_nongated(self, x, topk_ids, topk_weights, bufs, path, split, tiles, depth,
                           staging, workspace, stream, steps, shared_weights) -> MoEBuffers:
