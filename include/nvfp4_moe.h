@@ -566,7 +566,8 @@ typedef enum {
  * with the best group scores stay (without a bias and with group_top 1 the best
  * logit is a group's score, with group_top 2 the sum of its two best scores);
  * then the topk best choice values, compared exactly (values that FP32 cannot
- * order are ordered in FP64), ties to the lower index.  An expert whose logit is
+ * order are ordered in FP64; two that differ by no more than its rounding may
+ * stand in either order), ties to the lower index.  An expert whose logit is
  * -infinity or NaN, or whose bias is, cannot be chosen (a masked expert; an
  * all-masked row is a padding token); a logit of +infinity counts as the
  * largest finite one.  Slots that no expert can fill hold id -1 and weight 0:

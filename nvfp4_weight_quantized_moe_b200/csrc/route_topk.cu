@@ -523,15 +523,24 @@ NVM_DEV void select_experts(const RouteArgs& a, const T* row, const float (&l)[E
     if (scored) {
       if (lane < n) picks.ranked[rank] = c;
       __syncwarp();
+      uint2 p{}, q{};
       bool near = false;
-      if (lane + 1 < n && lane < a.topk) {
-        const uint2 p = picks.ranked[lane], q = picks.ranked[lane + 1];
+      if (lane + 1 < n) {
+        p = picks.ranked[lane], q = picks.ranked[lane + 1];
         const float v = key_value(p.x, 0.0f);
         near = v - key_value(q.x, 0.0f) <= bound(v);
-        // Equal logits and biases are equal in any arithmetic.
-        if (near && p.x == q.x) near = row[p.y] != row[q.y] || a.bias[p.y] != a.bias[q.y];
       }
-      if (__any_sync(kFull, near)) rank_exactly<T>(a, row, scores_exactly<T>(a, row, lmax), n, picks);
+      const unsigned nears = __ballot_sync(kFull, near);
+      if (nears & ((2u << (a.topk - 1)) - 1u)) {
+        // Equal logits and biases are equal in any arithmetic.  The order counts up to the
+        // topk-th candidate and through those that are the same as it: what is near to
+        // one of them may stand before all of them.
+        const bool same = near && p.x == q.x && row[p.y] == row[q.y] && a.bias[p.y] == a.bias[q.y];
+        const unsigned sames = __ballot_sync(kFull, same);
+        const int last = a.topk - 2 + __ffs(~(sames >> (a.topk - 1)));
+        if (nears & ~sames & ((2u << last) - 1u))
+          rank_exactly<T>(a, row, scores_exactly<T>(a, row, lmax), n, picks);
+      }
     }
     __syncwarp();
     return;
