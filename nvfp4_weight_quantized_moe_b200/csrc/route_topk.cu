@@ -398,11 +398,12 @@ NVM_DEV void select_experts(const RouteArgs& a, const T* row, const float (&l)[E
     }
     // A score is off by its values' errors and, for a sum, its own rounding: all of them
     // by the values' sizes, which a sum of opposite signs does not show.
-    uint32_t rest = group_key<float>(a, two);
-    const float v = key_value(rest, 0.0f);
     const bool sum = is_sum<float>(a, two);
-    const float size = fabsf(key_value(two.one, 0.0f)) + (sum ? fabsf(key_value(two.two, 0.0f)) : 0.0f);
-    const float off = ((sum ? unit : 0.5f * unit) + (sum ? size + fabsf(v) : size) * 0x1p-24f) * 0x1.00001p0f;
+    const float one = key_value(two.one, 0.0f), other = sum ? key_value(two.two, 0.0f) : 0.0f;
+    const float v = sum ? finite_sum(one, other) : one;
+    uint32_t rest = sum ? order_key(v) : two.one;
+    const float of_size = sums ? 0x1.00001p-23f : 0x1.00001p-24f, of_score = sums ? unit : 0.5f * unit;
+    const float off = two.one > kNone ? fmaf(fabsf(one) + fabsf(other), of_size, of_score) : 0.0f;
     // The best groups one after another.
     uint32_t worst = 0;
     mask = 0;
@@ -415,17 +416,20 @@ NVM_DEV void select_experts(const RouteArgs& a, const T* row, const float (&l)[E
       if (lane == at) rest = 0;
       worst = top;
     }
-    // FP32 has settled it if the least that a kept group's score can be is above the most
-    // that a left one's can (there may be none), both as distances from the worst kept
-    // one's: exact where they are small (2^-20 in `off` covers the ends' rounding).  What is
-    // not finite may be anywhere.
     if (scored || sums) {
-      const float from = v - key_value(worst, 0.0f);
-      const bool bounded = off < INFINITY;
-      const uint32_t least = (mask >> lane) & 1u ? order_key(bounded ? from - off : -INFINITY) : 0xffffffffu;
-      const uint32_t most = rest > kNone ? order_key(bounded ? from + off : INFINITY) : 0u;
-      if (__reduce_min_sync(kFull, least) <= __reduce_max_sync(kFull, most))
-        mask = groups_exactly<T, EPL>(a, row, scores_exactly<T>(a, row, lmax));
+      const uint32_t below = __reduce_max_sync(kFull, rest);  // there may be none
+      const float from = key_value(worst, 0.0f), gap = from - key_value(below, 0.0f);
+      const float most_off = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(off)));
+      if (below > kNone && !(gap > 2.00001f * most_off)) {
+        // Is the least that any kept group's score can be under the most that a left one's
+        // can?  Both as distances from the worst kept one's, exact where they are small;
+        // what is not finite may be anywhere.
+        const bool bounded = off < INFINITY;
+        const uint32_t least = (mask >> lane) & 1u ? order_key(bounded ? v - from - off : -INFINITY) : 0xffffffffu;
+        const uint32_t most = rest > kNone ? order_key(bounded ? v - from + off : INFINITY) : 0u;
+        if (__reduce_min_sync(kFull, least) <= __reduce_max_sync(kFull, most))
+          mask = groups_exactly<T, EPL>(a, row, scores_exactly<T>(a, row, lmax));
+      }
     }
     if (a.group_lanes > 0) {
       const uint32_t stays = (mask >> (lane / a.group_lanes)) & 1u ? 0xffffffffu : 0u;
