@@ -119,6 +119,7 @@ struct TcCfg {
   static constexpr int CTAS_PER_SM = kSmemPerSM / (SMEM + kSmemReservedPerCta);
   static_assert(B_PLANE_BYTES % 1024 == 0 && kWSlotBytes % 1024 == 0, "TMA tiles stay 1024-byte aligned");
   static_assert(TMEM_COLS <= 512, "TMEM budget");
+  static_assert(tc_smem_safe(SMEM, TMEM_COLS), "no pairs of two kernels wait for each other's tensor memory");
   static_assert(SB % CG == 0 && (kTileK / kStageK) % CG == 0, "commit groups tile the stages");
   static_assert(SB >= SA, "mma_done also tracks the A ring");
   // Every CTA that shared memory lets share an SM must find its TMEM columns

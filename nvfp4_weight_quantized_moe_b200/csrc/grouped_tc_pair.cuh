@@ -89,7 +89,10 @@ struct PairCfg {
   static constexpr int NBAR = 2 * WS + 2 * SB + SA + 2 * ND;
   static constexpr int OFF_TMEM = OFF_BAR + 8 * NBAR;
   static constexpr int OFF_ABORT = OFF_TMEM + 16;
-  static constexpr int SMEM = OFF_ABORT + 16 + 1024;
+  static constexpr int USED = OFF_ABORT + 16 + 1024;
+  // The 192-row passes use 152 KB of shared memory and all of the tensor memory.
+  static constexpr int SMEM = TMEM_COLS == 512 && USED < kAloneTcSmem ? kAloneTcSmem : USED;
+  static_assert(tc_smem_safe(SMEM, TMEM_COLS), "no pairs of two kernels wait for each other's tensor memory");
   static_assert(ND * D_COLS + (SMEM_A ? 0 : SA * A_COLS) <= (int)TMEM_COLS && SA >= 2, "TMEM budget");
   static_assert(!SMEM_A || (MODE != kModeDown && CTAS_PER_SM == 1), "A in shared memory: gate+up / up+activation");
   static_assert(B_PLANE_BYTES % 1024 == 0 && kPairWSlot % 1024 == 0, "TMA tiles stay 1024-byte aligned");

@@ -200,6 +200,7 @@ struct TileCfg {
   // Two CTAs of this size are all an SM holds, with anything that shares it: no
   // allocation of tensor memory ever waits for another cluster's.
   static_assert((DEEP ? 2 : 3) * (SMEM + 1024) > 228 * 1024 && 2 * BN <= 512, "tensor memory");
+  static_assert(tc_smem_safe(SMEM, BN), "no pairs of two kernels wait for each other's tensor memory");
 };
 
 constexpr int kTileThreads = 192;  // warp 0 loads, warp 1 issues, warps 2-5 drain
@@ -472,6 +473,7 @@ struct PairCfg8 {
   static constexpr int SMEM = OFF_ABORT + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(2 * (SMEM + 1024) > 228 * 1024, "one CTA per SM: it takes all of its tensor memory");
+  static_assert(tc_smem_safe(SMEM, 512), "no pairs of two kernels wait for each other's tensor memory");
 };
 
 }  // namespace

@@ -21,6 +21,17 @@ inline cudaError_t read_error_word(const void* symbol, int* value, bool clear) {
   return cudaMemcpyToSymbol(symbol, &zero, sizeof(int));
 }
 
+// Tensor memory is allocated by waiting for free columns.  Where CTA pairs of two
+// kernels (two streams) share the SMs and need more than the 512 columns together, one
+// pair may hold what the other waits for on one SM and wait for the other's on the
+// second, for good.  So a kernel that takes all columns asks for so much shared memory
+// that no other kernel with tensor memory fits beside it: all of them take kLeastTcSmem
+// at least (of 228 KB an SM, 1 KB a CTA reserved).  The others' columns fit together
+// wherever their shared memory and registers do.
+constexpr int kLeastTcSmem = 70 * 1024;
+constexpr int kAloneTcSmem = 228 * 1024 - 2 * 1024 - kLeastTcSmem + 1024;
+constexpr bool tc_smem_safe(int smem, int columns) { return smem >= (columns >= 512 ? kAloneTcSmem : kLeastTcSmem); }
+
 NVM_DEV uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
 // ---------------------------------------------------------------------------
