@@ -367,7 +367,9 @@ class NVFP4MoE:
                        bufs: Optional[MoEBuffers] = None, stream=None, **options) -> MoEBuffers:
         """:meth:`forward` from the router's logits [M, E] (bf16 or f32): the routing is one
         more launch, its result in ``bufs.routed_ids`` / ``bufs.routed_weights`` (first M
-        rows).  A token whose logits are all -inf (padding) adds nothing to ``out``.
+        rows).  A token whose logits are all -inf (padding) gets nothing from the routed
+        experts: its row of ``out`` is 0, or the shared expert's output times its entry of
+        ``shared_weights`` (0 for none).
         ``options`` as for :meth:`forward`."""
         m = x.shape[0]
         if tuple(logits.shape) != (m, self.num_experts):
