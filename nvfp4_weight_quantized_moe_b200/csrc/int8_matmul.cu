@@ -15,9 +15,10 @@
 // takes the channels as rows and the tokens as columns.  A lane loads 16
 // consecutive bytes of a row where the instruction wants four runs of four: the
 // k order inside a chunk is permuted, identically for both operands, which a sum
-// does not notice.  Bound by the weights' way from memory: 1 x 4096 x 2048 2.7 us
-// (8.4 MB, of which 1.3 us are the launch), 1 x 8192 x 4096 from HBM 13 us with DRAM at
-// 32 %: 16 rows of 64 bytes per load instruction, at most 98 KB in flight per SM.
+// does not notice.  Bound by the weights' way from memory: 1 x 4096 x 2048 (tokens, n, k)
+// 2.7 us with its 8.4 MB of weights in the L2 and 3.5 from HBM (1.3 us are the launch),
+// 1 x 5120 x 4096 4.9 and 7.3: 16 rows of 64 bytes per load instruction, at most 98 KB in
+// flight per SM.
 
 #include <cmath>
 
@@ -153,7 +154,9 @@ cudaError_t launch_reg(const Int8MatmulArgs& a, bool deep, cudaStream_t stream) 
 // stage of K, bytes through the L2 at a rate, an epilogue); the numbers are a
 // fit to 446 shapes of 1 to 8192 tokens, n 64 to 8192, k 128 to 8192, measured on
 // B200 in all nine forms.  Over those shapes the choice is 1.2 % slower than the
-// best form in the geometric mean; each of the nine is the best for some.
+// best form in the geometric mean; each of the nine is the best for some.  Three
+// sets of weights took turns, so those under 40 MB came from the L2: for a few tokens
+// with weights from HBM the estimates are low (1 x 5120 x 4096: 4.9 us, from HBM 7.3).
 struct Form {
   int bn;       // 0: register-fed; 64, 128: tiles of so many channels; 256: CTA pairs
   uint32_t by;  // register-fed: 8-token tiles; tiles: CTAs that split K

@@ -21,8 +21,8 @@
 // so topk <= 32 and num_groups <= 32.
 //
 // The work is one read of the logits (8191 x 256 FP32: 1.4 us at the copy
-// bandwidth); what bounds it is instruction issue, about 890 warp instructions a
-// token with scores, bias and groups (8191 x 256: 13 us, 68 % of the issue slots),
+// bandwidth); what bounds it is instruction issue, about 910 warp instructions a
+// token with scores, bias and groups (8191 x 256: 13 us, 70 % of the issue slots),
 // 600 without (8192 x 128 BF16: 7.7 us), and for one token the chain of warp
 // reductions (2.0 us and 3.5 us with groups, of which 1.3 us are the launch).
 
